@@ -1,7 +1,8 @@
 """GPTQ layer quantizer for AMD Instinct MI355X (gfx950).
 
 A thin Python binding over the C ABI of ``libgptq.so`` (declared in
-``include/gptq.h``).  The functions carry the C names; they only marshal
+``include/gptq.h``; the attention operators, ``include/gptq_attn.h``, are bound
+in ``attn.py`` and exported here).  The functions carry the C names; they only marshal
 arguments -- device pointers and the current HIP stream of PyTorch-ROCm
 tensors -- and raise ``GptqError`` on a non-zero status.  Every step of the
 quantizer runs in the library's HIP kernels; there is no other code path.
@@ -102,6 +103,7 @@ def lib():
     L.gptq_version.restype = ctypes.c_int
     L.gptq_trace_set.argtypes = [vp]
     L.gptq_trace_set.restype = ctypes.c_int
+    attn.bind(L)
     _lib = L
     return L
 
@@ -393,3 +395,9 @@ def quantize(W, H, params: Params, stream=None, want_what=True):
     gptq_quantize_layer(W, H, params, out["codes"], out["scales"], out["zeros"], out["w_hat"], out["row_loss"],
                         stream=stream)
     return out
+
+
+from . import attn  # noqa: E402
+from .attn import (KVBatch, KVCache, Rope, gptq_kv_append, gptq_kv_attention,  # noqa: E402,F401
+                   gptq_kv_attention_workspace_bytes, gptq_kv_read, gptq_qk_norm_rope, gptq_qk_norm_rope_backward,
+                   gptq_qk_norm_rope_backward_workspace_bytes)
