@@ -1,99 +1,49 @@
-// Attention of new tokens over the paged 8-bit cache.
-//
-//   s_j = sm_scale sk_j (q . kc_j),  out = sum_j e^(s_j - m) sv_j vc_j / sum_j e^(s_j - m)
-//
-// One wave a query token and head: 64 tokens at a time, a lane a token for the
-// scores and a lane an element for the output, in fp32, with the running maximum
-// and sum of the softmax.
-#include "attn.h"
+// Attention over the paged 8-bit cache: which kernel takes a call, and how long
+// sequences are split.
+#include "kv_attend.h"
 
 namespace gptq {
 namespace {
 
-__device__ __forceinline__ int code_at(const int8_t* p) { return *p; }
+struct Plan {
+  int tile_rows, nsplit;
+  int64_t chunk;
+};
 
-template <bool BF16>
-__global__ __launch_bounds__(64) void k_kv_attend(KvAttention A, uint32_t max_new) {
-  __shared__ float q[256];
-  __shared__ float w[64];
-  uint32_t id = blockIdx.x;
-  const int h = (int)(id % (uint32_t)A.a.q_heads);
-  id /= (uint32_t)A.a.q_heads;
-  const int i = (int)(id % max_new), b = (int)(id / max_new);
-  const Seq s = load_seq(A.batch, b, A.d_status);
-  if (i >= s.n) return;
-  const int lane = threadIdx.x, dim = A.cache.dim, block = A.cache.block;
-  const int hk = h / (A.a.q_heads / A.cache.kv_heads);
-  const int64_t row = s.row + i;
-  for (int d = lane; d < dim; d += 64) q[d] = load1<BF16>(A.q, row * A.q_token + h * A.q_head + d);
-  __syncthreads();
-  const int64_t p = (int64_t)s.len - s.n + i;
-  int64_t end = A.a.causal && p + 1 < s.len ? p + 1 : s.len;
-  int64_t begin = A.a.window > 0 && p - A.a.window + 1 > 0 ? p - A.a.window + 1 : 0;
-  float m = -INFINITY, sum = 0.0f, acc[4] = {0, 0, 0, 0};
-  const int32_t* table = A.batch.block_table + b * A.batch.table_stride;
-  for (int64_t t0 = begin & ~63ll; t0 < end; t0 += 64) {
-    const int64_t j = t0 + lane;
-    float x = -INFINITY, vs = 0.0f;
-    int64_t page = 0;
-    if (j < end) {
-      page = table[j / block];
-      if (page < 0 || page >= A.cache.pages) {
-        raise_einval(A.d_status);
-        page = 0;
-      }
-    }
-    const int64_t slot = page * A.cache.kv_heads + hk;
-    if (j >= begin && j < end) {
-      const int8_t* k = A.cache.k_codes + (slot * block + j % block) * dim;
-      x = 0.0f;
-      for (int d = 0; d < dim; ++d) x = fmaf(q[d], (float)code_at(k + d), x);
-      x *= A.cache.k_scales[slot] * A.a.sm_scale;
-      vs = A.cache.v_scales[slot];
-    }
-    float mt = x;
-    for (int k = 1; k < 64; k *= 2) mt = fmaxf(mt, __shfl_xor(mt, k));
-    const float mn = fmaxf(m, mt);
-    const float e = j >= begin && j < end ? expf(x - mn) : 0.0f;
-    const float f = m == -INFINITY ? 0.0f : expf(m - mn);
-    float es = e;
-    for (int k = 1; k < 64; k *= 2) es += __shfl_xor(es, k);
-    sum = sum * f + es;
-    m = mn;
-    w[lane] = j >= begin && j < end ? e * vs : 0.0f;
-    __syncthreads();
-    for (int c = 0; c < 4; ++c) acc[c] *= f;
-    for (int64_t g = t0; g < t0 + 64 && g < end; g += 16) {
-      const int64_t pg = __shfl((int)page, (int)(g - t0));
-      const int8_t* v = A.cache.v_codes + (pg * A.cache.kv_heads + hk) * block * dim + g % block * dim;
-      for (int c = 0; 64 * c + lane < dim; ++c)
-        for (int k = 0; k < 16; ++k)
-          acc[c] = fmaf(w[g - t0 + k], (float)code_at(v + (64 * c + lane) * 16 + k), acc[c]);
-    }
-    __syncthreads();
-  }
-  for (int c = 0; 64 * c + lane < dim; ++c) {
-    const float o = sum > 0.0f || sum != sum ? acc[c] / sum : 0.0f;
-    const int64_t at = row * A.out_token + h * A.out_head + 64 * c + lane;
-    if (BF16)
-      static_cast<__bf16*>(A.out)[at] = (__bf16)o;
-    else
-      static_cast<float*>(A.out)[at] = o;
-  }
-  if (A.lse && lane == 0) A.lse[row * A.a.q_heads + h] = m + logf(sum);
+Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
+  Plan p;
+  p.tile_rows = rows > 16 && c.dim < 256 ? 32 : 16;
+  const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+  const int64_t base = b.batch * c.kv_heads * tiles;
+  // tokens a tile may see, with the rounding of its first
+  int64_t span = b.max_kv;
+  if (a.window > 0 && a.window + b.max_new < span) span = a.window + b.max_new;
+  span += 63;
+  const int64_t want = (1024 + base - 1) / base;
+  int64_t chunk = (span + want - 1) / want;
+  chunk = (chunk + 255) / 256 * 256;
+  p.chunk = chunk;
+  p.nsplit = (int)((span + chunk - 1) / chunk);
+  return p;
 }
 
 }  // namespace
 
-size_t kv_attention_workspace(const gptq_kv_cache&, const gptq_kv_batch&, bool, const gptq_attention&) { return 0; }
+size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool, const gptq_attention& a) {
+  const Plan p = make_plan(cache, batch, a);
+  if (p.nsplit <= 1) return 0;
+  return (size_t)batch.total * a.q_heads * p.nsplit * (cache.dim + 1) * sizeof(float);
+}
 
 hipError_t kv_attention(const KvAttention& a, hipStream_t stream) {
-  const uint32_t grid = (uint32_t)(a.batch.batch * a.batch.max_new * a.a.q_heads);
-  if (a.bf16)
-    k_kv_attend<true><<<grid, 64, 0, stream>>>(a, (uint32_t)a.batch.max_new);
-  else
-    k_kv_attend<false><<<grid, 64, 0, stream>>>(a, (uint32_t)a.batch.max_new);
-  return hipGetLastError();
+  const Plan p = make_plan(a.cache, a.batch, a.a);
+  Partials w{nullptr, nullptr, p.nsplit, p.chunk};
+  if (p.nsplit > 1) {
+    w.out = static_cast<float*>(a.workspace);
+    w.lse2 = w.out + (size_t)a.batch.total * a.a.q_heads * p.nsplit * a.cache.dim;
+  }
+  return kv_rows_launch(a, w, p.tile_rows, stream);
 }
 
 }  // namespace gptq

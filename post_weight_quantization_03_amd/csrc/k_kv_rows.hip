@@ -1,0 +1,396 @@
+// Attention of few query rows over the paged 8-bit cache: single tokens, guessed
+// tokens, short chunks.
+//
+// A row is a query token and head; the rows of a key head's group go together, 16
+// (or 32) at a time, as the columns of two matrix products on
+// v_mfma_f32_16x16x32_f16:  S^T = K Q^T,  O^T += V^T P^T.  Every cache byte is read
+// once a row tile, straight from HBM into the lane that needs it as an operand:
+// no LDS, no barrier in the loop.
+//   K: row m = lane % 16 of tile t is token 16 (m / 4) + 4 t + m % 4 of 64, so that
+//      in the product lane (q = l % 16, g = l / 16) holds tokens 16 g .. 16 g + 15 of
+//      row q, one scale group, in order; its 16-byte loads are elements 64 i + 16 g
+//      .. + 15, the k-slots of two MFMAs.
+//   V: lane (d = l % 16, g) loads tokens 16 g .. 16 g + 15 of element d in one piece
+//      (the cache's order), the k-slots of two MFMAs, which meet the same tokens of P
+//      in the same lane group: P never moves between lanes.
+// A wave goes through 64 tokens a turn, four waves side by side; the loads of the
+// next turn's K are issued when the scores are done, those of V when the output is,
+// so about 8 to 16 KB a wave is always on its way.  Each keeps its own maximum, sum
+// and output; they are joined in LDS at the end, and over the splits of a long
+// sequence by k_kv_join.
+//
+// Scales: K's multiplies the score.  V's enters the weight as its ratio to the
+// largest seen so far (like the running maximum), so fp16 weights keep their range
+// whatever the scales are.
+#include "kv_attend.h"
+
+namespace gptq {
+namespace {
+
+constexpr int KW = 4;  // waves
+
+template <int DIM, bool BF16, int CT>
+__global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAttention A, Partials P, uint32_t row_tiles) {
+  constexpr int NI = DIM / 64;  // 16-byte K loads a row
+  constexpr int NK = DIM / 32;  // MFMA steps of the first product
+  constexpr int ND = DIM / 16;  // d tiles
+  constexpr int CW = DIM < 128 ? DIM : 128;  // columns joined at a time
+  constexpr int LDO = CW + 4;
+  __shared__ __align__(16) float so[KW][16 * LDO];
+  __shared__ float sm[KW][16 * CT], sl[KW][16 * CT], sr[KW][16 * CT];
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n16 = lane & 15, g = lane >> 4;
+  uint32_t id = blockIdx.x;
+  const int split = (int)(id % (uint32_t)P.nsplit);
+  id /= (uint32_t)P.nsplit;
+  const int rt = (int)(id % row_tiles);
+  id /= row_tiles;
+  const int hk = (int)(id % (uint32_t)A.cache.kv_heads), b = (int)(id / (uint32_t)A.cache.kv_heads);
+  const Seq s = load_seq(A.batch, b, A.d_status);
+  const int group = A.a.q_heads / A.cache.kv_heads;
+  const int rows = s.n * group, r0 = rt * 16 * CT;
+  if (r0 >= rows) return;
+  const Span span = row_span(A, s, r0, 16 * CT, group);
+  const int64_t first = span.begin + split * P.chunk;
+  if (split > 0 && first >= span.end) return;
+  const bool whole = span.end - span.begin <= P.chunk;
+  const int64_t stop = first + P.chunk < span.end ? first + P.chunk : span.end;
+  const int32_t* table = A.batch.block_table + b * A.batch.table_stride;
+  const int shift = __builtin_ctz((unsigned)A.cache.block);
+  const int block = A.cache.block;
+
+  // queries, scaled to [2^7, 2^8) by row
+  f16x8 qh[CT][NK], ql[CT][BF16 ? 1 : NK];
+  float qs[CT];
+  Sees see[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int r = r0 + 16 * c + n16;
+    float x[NK][8];
+    float most = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[k][j] = 0.0f;
+      if (r < rows) {
+        const int64_t o = (s.row + r / group) * A.q_token + (hk * group + r % group) * A.q_head + 64 * (k >> 1) +
+                          16 * g + 8 * (k & 1);
+        if (A.vec)
+          load8<BF16, true>(A.q, o, x[k]);
+        else
+          load8<BF16, false>(A.q, o, x[k]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[k][j]));
+    }
+    most = fmaxf(most, __shfl_xor(most, 16));
+    most = fmaxf(most, __shfl_xor(most, 32));
+    float up, down;
+    row_scale(most, up, down);
+    qs[c] = A.a.sm_scale * 1.44269504088896340736f * down;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[k][j] *= up;
+      if constexpr (BF16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) qh[c][k][j] = (_Float16)x[k][j];
+      } else {
+        split16(x[k], qh[c][k], ql[c][k]);
+      }
+    }
+    see[c] = row_sees(A, s, r, group);
+  }
+  // tokens from full_lo to full_hi are seen by every row of the tile
+  int full_lo, full_hi;
+  {
+    const int last = (r0 + 16 * CT < rows ? r0 + 16 * CT : rows) - 1;
+    full_lo = row_sees(A, s, last, group).lo;
+    full_hi = row_sees(A, s, r0, group).hi;
+  }
+
+  f32x4 o[CT][ND];
+  float m[CT], l[CT], ref = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    m[c] = -INFINITY;
+    l[c] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[c][d] = (f32x4){0, 0, 0, 0};
+  }
+
+  u32x4v kr[4][NI], vr[ND];
+  float ks = 0.0f, vs = 0.0f;
+  auto slots = [&](int64_t t, int64_t& sk, int64_t& sv) {
+    sk = slot_at(A, table, t + 16 * (n16 >> 2), stop, shift, hk);
+    sv = slot_at(A, table, t + 16 * g, stop, shift, hk);
+  };
+  auto load_k = [&](int64_t t, int64_t sk, int64_t sv) {
+    const int off = (int)((t + 16 * (n16 >> 2)) & (block - 1)) + (n16 & 3);
+    const int8_t* p = A.cache.k_codes + (sk * block + off) * DIM + 16 * g;
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) kr[tt][i] = *reinterpret_cast<const u32x4v*>(p + 4 * tt * DIM + 64 * i);
+    ks = A.cache.k_scales[sv];
+  };
+  auto load_v = [&](int64_t t, int64_t sv) {
+    const int off = (int)((t + 16 * g) & (block - 1));
+    const int8_t* p = A.cache.v_codes + (sv * block + off) * DIM + 16 * n16;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) vr[d] = *reinterpret_cast<const u32x4v*>(p + 256 * d);
+    vs = A.cache.v_scales[sv];
+  };
+
+  int64_t t = first + 64 * wave;
+  int64_t sk = 0, sv = 0, sk1 = 0, sv1 = 0;
+  if (t < stop) {
+    slots(t, sk, sv);
+    load_k(t, sk, sv);
+    load_v(t, sv);
+    if (t + 64 * KW < stop) slots(t + 64 * KW, sk1, sv1);
+  }
+  for (; t < stop; t += 64 * KW) {
+    const int64_t tn = t + 64 * KW;
+    // scores
+    f32x4 x[CT][4];
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) x[c][tt] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const u32x4v w = kr[tt][k >> 1];
+        const f16x8 a = (k & 1) ? codes_to_f16(w[2], w[3]) : codes_to_f16(w[0], w[1]);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          x[c][tt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[c][k], x[c][tt], 0, 0, 0);
+          if constexpr (!BF16) x[c][tt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[c][k], x[c][tt], 0, 0, 0);
+        }
+      }
+    }
+    const float ks_now = ks;
+    float vs_now = t + 16 * g < stop ? vs : 0.0f;
+    if (tn < stop) load_k(tn, sk1, sv1);
+
+    // V's scales against the largest seen so far
+    float rt_max = fmaxf(vs_now, __shfl_xor(vs_now, 16));
+    rt_max = fmaxf(rt_max, __shfl_xor(rt_max, 32));
+    const float ref_new = fmaxf(ref, rt_max);
+    const float ref_inv = ref_new > 0.0f ? 1.0f / ref_new : 0.0f;
+    const float vratio = vs_now * ref_inv, oratio = ref * ref_inv;
+    ref = ref_new;
+
+    const bool full = t >= full_lo && t + 64 <= full_hi;
+    f16x8 ph[CT][2], pl[CT][BF16 ? 1 : 2];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const float f = ks_now * qs[c];
+      float most = -INFINITY;
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float y = x[c][tt][r] * f;
+          if (!full) {
+            const int j = (int)t + 16 * g + 4 * tt + r;
+            y = j >= see[c].lo && j < see[c].hi ? y : -INFINITY;
+          }
+          x[c][tt][r] = y;
+          most = fmaxf(most, y);
+        }
+      most = fmaxf(most, __shfl_xor(most, 16));
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const float mn = fmaxf(m[c], most);
+      const float base = mn == -INFINITY ? 0.0f : mn;
+      const float alpha = exp2_fast(m[c] - base);
+      m[c] = mn;
+      float sum = 0.0f;
+      float p[16];
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float y = x[c][tt][r];
+          const float e = exp2_fast(y - base + KV_PEXP);
+          sum += e;
+          float w = e * vratio;
+          if (!full) w = y == -INFINITY ? 0.0f : w;  // also where the block's scale is NaN
+          p[4 * tt + r] = w;
+        }
+      l[c] = l[c] * alpha + sum;
+      const float turn = alpha * oratio;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[c][d] *= turn;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float q8[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q8[j] = p[8 * u + j];
+        if constexpr (BF16) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ph[c][u][j] = (_Float16)q8[j];
+        } else {
+          split16(q8, ph[c][u], pl[c][u]);
+        }
+      }
+    }
+    // output
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f16x8 a = codes_to_f16(vr[d][2 * u], vr[d][2 * u + 1]);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[c][u], o[c][d], 0, 0, 0);
+          if constexpr (!BF16) o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[c][u], o[c][d], 0, 0, 0);
+        }
+      }
+    if (tn < stop) {
+      load_v(tn, sv1);
+      sk = sk1, sv = sv1;
+      if (tn + 64 * KW < stop) slots(tn + 64 * KW, sk1, sv1);
+    }
+  }
+
+  // join the waves
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    l[c] += __shfl_xor(l[c], 16);
+    l[c] += __shfl_xor(l[c], 32);
+    if (g == 0) sm[wave][16 * c + n16] = m[c], sl[wave][16 * c + n16] = l[c], sr[wave][16 * c + n16] = ref;
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int h = 0; h < DIM / CW; ++h) {
+      __syncthreads();
+#pragma unroll
+      for (int d = 0; d < CW / 16; ++d)
+        *reinterpret_cast<f32x4*>(&so[wave][n16 * LDO + 16 * d + 4 * g]) = o[c][h * (CW / 16) + d];
+      __syncthreads();
+      for (int i = threadIdx.x; i < 16 * CW / 8; i += 64 * KW) {
+        const int row = i / (CW / 8), d = 8 * (i % (CW / 8));
+        const int r = r0 + 16 * c + row;
+        if (r >= rows) continue;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) mm = fmaxf(mm, sm[w][16 * c + row]);
+        const float base = mm == -INFINITY ? 0.0f : mm;
+        float sum = 0.0f, y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const float f = exp2_fast(sm[w][16 * c + row] - base);
+          const float fo = f * sr[w][16 * c + row];
+          sum = fmaf(f, sl[w][16 * c + row], sum);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = fmaf(fo, so[w][row * LDO + d + j], y[j]);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a sum of NaN stays NaN
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= inv;
+        const float lse2 = sum == 0.0f ? -INFINITY : mm + __log2f(sum) - KV_PEXP;
+        const int64_t token = s.row + r / group;
+        const int head = hk * group + r % group;
+        if (whole) {
+          const int64_t at = token * A.out_token + head * A.out_head + h * CW + d;
+          if (A.vec)
+            store8<BF16, true>(A.out, at, y);
+          else
+            store8<BF16, false>(A.out, at, y);
+          if (A.lse && h == 0 && d == 0) A.lse[token * A.a.q_heads + head] = lse2 * 0.69314718055994530942f;
+        } else {
+          const int64_t at = (token * A.a.q_heads + head) * P.nsplit + split;
+          store8<false, true>(P.out, at * DIM + h * CW + d, y);
+          if (h == 0 && d == 0) P.lse2[at] = lse2;
+        }
+      }
+    }
+}
+
+// Joins the splits of each row that has several: out = sum 2^(lse2_s - max) out_s /
+// sum 2^(lse2_s - max).  A wave a row and head.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttention A, Partials P, uint32_t tile_rows) {
+  const int lane = threadIdx.x & 63;
+  uint32_t id = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int h = (int)(id % (uint32_t)A.a.q_heads);
+  id /= (uint32_t)A.a.q_heads;
+  const int i = (int)(id % (uint32_t)A.batch.max_new);
+  const int64_t b = id / (uint32_t)A.batch.max_new;
+  if (b >= A.batch.batch) return;
+  const Seq s = load_seq(A.batch, (int)b, nullptr);
+  if (i >= s.n) return;
+  const int group = A.a.q_heads / A.cache.kv_heads, dim = A.cache.dim;
+  const int r = i * group + h % group;
+  const Span span = row_span(A, s, r / (int)tile_rows * (int)tile_rows, (int)tile_rows, group);
+  const int ns = (int)((span.end - span.begin + P.chunk - 1) / P.chunk);
+  if (ns <= 1) return;
+  const int64_t token = s.row + i, at = (token * A.a.q_heads + h) * P.nsplit;
+  float mm = -INFINITY;
+  for (int k = lane; k < ns; k += 64) mm = fmaxf(mm, P.lse2[at + k]);
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) mm = fmaxf(mm, __shfl_xor(mm, k));
+  const float base = mm == -INFINITY ? 0.0f : mm;
+  float sum = 0.0f, y[4] = {0, 0, 0, 0};
+  const int per = dim / 64;
+#pragma unroll 4
+  for (int k = 0; k < ns; ++k) {
+    const float f = exp2_fast(P.lse2[at + k] - base);
+    sum += f;
+    const float* p = P.out + (at + k) * dim + per * lane;
+    for (int e = 0; e < per; ++e) y[e] = fmaf(f, p[e], y[e]);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t o = token * A.out_token + h * A.out_head + per * lane;
+  for (int e = 0; e < per; ++e) {
+    if constexpr (BF16)
+      static_cast<__bf16*>(A.out)[o + e] = (__bf16)(y[e] * inv);
+    else
+      static_cast<float*>(A.out)[o + e] = y[e] * inv;
+  }
+  if (A.lse && lane == 0)
+    A.lse[token * A.a.q_heads + h] = (sum == 0.0f ? -INFINITY : mm + __log2f(sum)) * 0.69314718055994530942f;
+}
+
+template <int DIM, bool BF16>
+hipError_t launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
+  const int64_t rows = a.batch.max_new * (a.a.q_heads / a.cache.kv_heads);
+  const uint32_t tiles = (uint32_t)((rows + tile_rows - 1) / tile_rows);
+  const uint32_t grid = (uint32_t)(a.batch.batch * a.cache.kv_heads * tiles * p.nsplit);
+  if constexpr (DIM < 256) {
+    if (tile_rows == 32)
+      k_kv_rows<DIM, BF16, 2><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
+    else
+      k_kv_rows<DIM, BF16, 1><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
+  } else {
+    k_kv_rows<DIM, BF16, 1><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
+  }
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  if (p.nsplit > 1) {
+    const uint32_t waves = (uint32_t)(a.batch.batch * a.batch.max_new * a.a.q_heads);
+    k_kv_join<BF16><<<(waves + 3) / 4, 256, 0, stream>>>(a, p, (uint32_t)tile_rows);
+  }
+  return hipGetLastError();
+}
+
+template <int DIM>
+hipError_t launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
+  return a.bf16 ? launch<DIM, true>(a, p, tile_rows, stream) : launch<DIM, false>(a, p, tile_rows, stream);
+}
+
+}  // namespace
+
+hipError_t kv_rows_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
+  switch (a.cache.dim) {
+    case 64: return launch<64>(a, p, tile_rows, stream);
+    case 128: return launch<128>(a, p, tile_rows, stream);
+    default: return launch<256>(a, p, tile_rows, stream);
+  }
+}
+
+}  // namespace gptq
