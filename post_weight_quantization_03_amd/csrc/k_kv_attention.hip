@@ -13,14 +13,17 @@ struct Plan {
 Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
   Plan p;
-  p.tile_rows = rows > 16 && c.dim < 256 ? 32 : 16;
+  if (rows <= 64)
+    p.tile_rows = rows > 16 && c.dim < 256 ? 32 : 16;
+  else
+    p.tile_rows = rows > 128 && c.dim < 256 ? 256 : 128;
   const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   const int64_t base = b.batch * c.kv_heads * tiles;
   // tokens a tile may see, with the rounding of its first
   int64_t span = b.max_kv;
   if (a.window > 0 && a.window + b.max_new < span) span = a.window + b.max_new;
   span += 63;
-  const int64_t want = (1024 + base - 1) / base;
+  const int64_t want = ((p.tile_rows >= 128 ? 512 : 1024) + base - 1) / base;
   int64_t chunk = (span + want - 1) / want;
   chunk = (chunk + 255) / 256 * 256;
   p.chunk = chunk;
@@ -43,7 +46,9 @@ hipError_t kv_attention(const KvAttention& a, hipStream_t stream) {
     w.out = static_cast<float*>(a.workspace);
     w.lse2 = w.out + (size_t)a.batch.total * a.a.q_heads * p.nsplit * a.cache.dim;
   }
-  return kv_rows_launch(a, w, p.tile_rows, stream);
+  const hipError_t e = p.tile_rows >= 128 ? kv_prompt_launch(a, w, p.tile_rows, stream)
+                                          : kv_rows_launch(a, w, p.tile_rows, stream);
+  return e == hipSuccess && p.nsplit > 1 ? kv_join_launch(a, w, p.tile_rows, stream) : e;
 }
 
 }  // namespace gptq

@@ -370,11 +370,6 @@ hipError_t launch(const KvAttention& a, const Partials& p, int tile_rows, hipStr
   } else {
     k_kv_rows<DIM, BF16, 1><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
   }
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  if (p.nsplit > 1) {
-    const uint32_t waves = (uint32_t)(a.batch.batch * a.batch.max_new * a.a.q_heads);
-    k_kv_join<BF16><<<(waves + 3) / 4, 256, 0, stream>>>(a, p, (uint32_t)tile_rows);
-  }
   return hipGetLastError();
 }
 
@@ -391,6 +386,15 @@ hipError_t kv_rows_launch(const KvAttention& a, const Partials& p, int tile_rows
     case 128: return launch<128>(a, p, tile_rows, stream);
     default: return launch<256>(a, p, tile_rows, stream);
   }
+}
+
+hipError_t kv_join_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
+  const uint32_t waves = (uint32_t)(a.batch.batch * a.batch.max_new * a.a.q_heads);
+  if (a.bf16)
+    k_kv_join<true><<<(waves + 3) / 4, 256, 0, stream>>>(a, p, (uint32_t)tile_rows);
+  else
+    k_kv_join<false><<<(waves + 3) / 4, 256, 0, stream>>>(a, p, (uint32_t)tile_rows);
+  return hipGetLastError();
 }
 
 }  // namespace gptq

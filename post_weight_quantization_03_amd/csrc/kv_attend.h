@@ -109,6 +109,11 @@ struct Partials {
   int64_t chunk;
 };
 
-hipError_t kv_rows_launch(const KvAttention& a, const Partials& p, int row_tiles, hipStream_t stream);
+// k_kv_rows.hip: row tiles of 16 or 32 (dim 256: 16).
+hipError_t kv_rows_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream);
+// Joins the splits (k_kv_rows.hip).
+hipError_t kv_join_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream);
+// k_kv_prompt.hip: row tiles of 128 or 256 (dim 256: 128).
+hipError_t kv_prompt_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream);
 
 }  // namespace gptq
