@@ -17,6 +17,8 @@ Modules
   hadamard_ref  the fixed randomised Hadamard rotation Q and W Q, Q^T H Q.
   qep_ref     the error-propagation correction of W from full-precision and
               quantized-model inputs, before GPTQ.
+  attn_ref    the attention operators: per-head norm and position rotation with
+              their gradients, the paged 8-bit cache, attention over it.
 
 Parity pins: every function here is checked in ``tests/test_oracle_*.py``
 against closed forms, the hand-worked 4x8 example in ``tests/golden``,

@@ -9,7 +9,8 @@ namespace {
 using namespace gptq;
 
 constexpr int64_t MAX_DIM = (int64_t)1 << 30;
-constexpr int64_t MAX_GRID = INT32_MAX;
+constexpr int64_t MAX_WORK = INT32_MAX;             // lanes of the norm and rotation, counted in 32 bits
+constexpr int64_t MAX_GRID = ((int64_t)1 << 24) - 1;  // workgroups of 256 threads: fewer than 2^32 threads a launch
 
 bool dtype_ok(gptq_dtype dt) { return dt == GPTQ_BF16 || dt == GPTQ_F32; }
 int64_t elem_size(gptq_dtype dt) { return dt == GPTQ_BF16 ? 2 : 4; }
@@ -58,15 +59,16 @@ bool batch_pointers(const gptq_kv_batch* b) {
 }
 
 // The heads of one side in a norm-and-rotation call, forward (y) or backward (dy, dx).
-int side_check(const gptq_heads* s, gptq_dtype dt, HeadSide* out, bool* vec) {
+// Without tokens no element is pointed at.
+int side_check(const gptq_heads* s, gptq_dtype dt, bool any, HeadSide* out, bool* vec) {
   *out = HeadSide{};
   if (!s || s->heads == 0) return GPTQ_OK;
-  if (s->heads < 0 || s->heads > 65536 || !s->x || !s->y) return GPTQ_EINVAL;
+  if (s->heads < 0 || s->heads > 65536 || (any && (!s->x || !s->y))) return GPTQ_EINVAL;
   if (!stride_ok(s->x_token) || !stride_ok(s->x_head) || !stride_ok(s->y_token) || !stride_ok(s->y_head))
     return GPTQ_EINVAL;
   const uintptr_t a = (uintptr_t)elem_size(dt);
   if (!aligned(s->x, a) || !aligned(s->y, a) || !aligned(s->weight, a)) return GPTQ_EINVAL;
-  if (s->x == s->y && (s->x_token != s->y_token || s->x_head != s->y_head)) return GPTQ_EINVAL;
+  if (any && s->x == s->y && (s->x_token != s->y_token || s->x_head != s->y_head)) return GPTQ_EINVAL;
   *vec = *vec && vec_ok(s->x, s->x_token, s->x_head, dt) && vec_ok(s->y, s->y_token, s->y_head, dt) &&
          aligned(s->weight, 16);
   out->x = s->x, out->x_token = s->x_token, out->x_head = s->x_head;
@@ -74,10 +76,10 @@ int side_check(const gptq_heads* s, gptq_dtype dt, HeadSide* out, bool* vec) {
   out->weight = s->weight, out->heads = s->heads;
   return GPTQ_OK;
 }
-int side_check(const gptq_heads_grad* s, gptq_dtype dt, HeadSide* out, bool* vec) {
+int side_check(const gptq_heads_grad* s, gptq_dtype dt, bool any, HeadSide* out, bool* vec) {
   *out = HeadSide{};
   if (!s || s->heads == 0) return GPTQ_OK;
-  if (s->heads < 0 || s->heads > 65536 || !s->dy || !s->dx || (s->weight && !s->x)) return GPTQ_EINVAL;
+  if (s->heads < 0 || s->heads > 65536 || (any && (!s->dy || !s->dx || (s->weight && !s->x)))) return GPTQ_EINVAL;
   if (!stride_ok(s->dy_token) || !stride_ok(s->dy_head) || !stride_ok(s->dx_token) || !stride_ok(s->dx_head) ||
       (s->weight && (!stride_ok(s->x_token) || !stride_ok(s->x_head))))
     return GPTQ_EINVAL;
@@ -85,8 +87,8 @@ int side_check(const gptq_heads_grad* s, gptq_dtype dt, HeadSide* out, bool* vec
   if (!aligned(s->dy, a) || !aligned(s->dx, a) || !aligned(s->weight, a) || (s->weight && !aligned(s->x, a)) ||
       !aligned(s->dweight, 4))
     return GPTQ_EINVAL;
-  if (s->dy == s->dx && (s->dy_token != s->dx_token || s->dy_head != s->dx_head)) return GPTQ_EINVAL;
-  if (s->weight && s->x == s->dx) return GPTQ_EINVAL;
+  if (any && s->dy == s->dx && (s->dy_token != s->dx_token || s->dy_head != s->dx_head)) return GPTQ_EINVAL;
+  if (any && s->weight && s->x == s->dx) return GPTQ_EINVAL;
   *vec = *vec && vec_ok(s->dy, s->dy_token, s->dy_head, dt) && vec_ok(s->dx, s->dx_token, s->dx_head, dt) &&
          aligned(s->weight, 16) && (!s->weight || vec_ok(s->x, s->x_token, s->x_head, dt));
   out->dy = s->dy, out->dy_token = s->dy_token, out->dy_head = s->dy_head;
@@ -105,13 +107,13 @@ int norm_rope_args(const Heads* q, const Heads* k, gptq_dtype dt, int64_t tokens
   if (st != GPTQ_OK) return st;
   *a = NormRope{};
   bool vec = true;
-  if ((st = side_check(q, dt, &a->q, &vec)) != GPTQ_OK) return st;
-  if ((st = side_check(k, dt, &a->k, &vec)) != GPTQ_OK) return st;
+  if ((st = side_check(q, dt, tokens > 0, &a->q, &vec)) != GPTQ_OK) return st;
+  if ((st = side_check(k, dt, tokens > 0, &a->k, &vec)) != GPTQ_OK) return st;
   if (tokens > 0 && a->q.heads + a->k.heads > 0 && rope->rot > 0 && (!positions || !aligned(positions, 4)))
     return GPTQ_EINVAL;
   if (!aligned(d_status, 4)) return GPTQ_EINVAL;
   // an item (token and heads) and a thread of it are counted in 32 bits
-  if (tokens * ((int64_t)a->q.heads + a->k.heads) > MAX_GRID / head_lanes(dim)) return GPTQ_EUNSUPPORTED;
+  if (tokens * ((int64_t)a->q.heads + a->k.heads) > MAX_WORK / head_lanes(dim)) return GPTQ_EUNSUPPORTED;
   a->bf16 = dt == GPTQ_BF16;
   a->vec = vec;
   a->tokens = tokens;
@@ -251,7 +253,7 @@ int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, co
     return GPTQ_EINVAL;
   // with no token in any sequence no page exists to be pointed at
   if (batch->max_kv > 0 && (st = cache_pointers(cache)) != GPTQ_OK) return st;
-  if (batch->batch * batch->max_new > MAX_GRID / (int64_t)att->q_heads) return GPTQ_EUNSUPPORTED;
+  if (!kv_attention_fits(*cache, *batch, *att)) return GPTQ_EUNSUPPORTED;
   const size_t need = kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, *att);
   if (workspace_bytes < need || (need > 0 && !workspace)) return GPTQ_EWORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return GPTQ_EINVAL;

@@ -39,6 +39,15 @@ size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& b
   return (size_t)batch.total * a.q_heads * p.nsplit * (cache.dim + 1) * sizeof(float);
 }
 
+bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  const int64_t limit = ((int64_t)1 << 32) - 1;
+  if (b.batch * b.max_new > limit / 64 / a.q_heads) return false;  // a wave a row and head where splits are joined
+  const Plan p = make_plan(c, b, a);
+  const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
+  const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+  return b.batch * c.kv_heads * tiles * p.nsplit <= limit / (p.tile_rows == 256 ? 512 : 256);
+}
+
 hipError_t kv_attention(const KvAttention& a, hipStream_t stream) {
   const Plan p = make_plan(a.cache, a.batch, a.a);
   Partials w{nullptr, nullptr, p.nsplit, p.chunk};

@@ -182,7 +182,8 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
       const float lr = keep_nan_max(lv - run_ref, P_RATIO_MIN);
       sc[buf].ks[threadIdx.x] = next_ks;
       sc[buf].lr[threadIdx.x] = lr;
-      sc[buf].ir[threadIdx.x] = exp2_fast(-lr);
+      // with a scale of NaN the weights that see it are NaN; the sums of rows that do not are 0
+      sc[buf].ir[threadIdx.x] = lr != lr ? 1.0f : exp2_fast(-lr);
       if (threadIdx.x == 0) sc[buf].lref = run_ref;
     }
   };
