@@ -23,7 +23,7 @@ Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attent
   int64_t span = b.max_kv;
   if (a.window > 0 && a.window + b.max_new < span) span = a.window + b.max_new;
   span += 63;
-  const int64_t want = ((p.tile_rows >= 128 ? 512 : 1024) + base - 1) / base;
+  const int64_t want = (512 + base - 1) / base;
   int64_t chunk = (span + want - 1) / want;
   chunk = (chunk + 255) / 256 * 256;
   p.chunk = chunk;
@@ -41,8 +41,9 @@ size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& b
 
 bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   const int64_t limit = ((int64_t)1 << 32) - 1;
-  if (b.batch * b.max_new > limit / 64 / a.q_heads) return false;  // a wave a row and head where splits are joined
   const Plan p = make_plan(c, b, a);
+  // a workgroup a row and head where splits are joined
+  if (p.nsplit > 1 && b.batch * b.max_new > limit / 256 / a.q_heads) return false;
   const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
   const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   return b.batch * c.kv_heads * tiles * p.nsplit <= limit / (p.tile_rows == 256 ? 512 : 256);

@@ -28,6 +28,7 @@ namespace gptq {
 namespace {
 
 constexpr int PT = 64;                // tokens a tile
+constexpr int SB = 8;                 // tiles whose scales are brought in together
 constexpr float P_EXP = 6.0f;         // weights are 2^P_EXP e^(s - m), m up to 2^P_SLACK behind the maximum
 constexpr float P_SLACK = 8.0f;
 constexpr float P_LOG_MIN = -200.0f;  // log2 of a value scale, at least
@@ -55,7 +56,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   struct Scales {
     float ks[4], lr[4], ir[4], lref, pad[3];
   };
-  __shared__ __align__(16) Scales sc[2];
+  __shared__ __align__(16) Scales sc[2 * SB];
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 31, half = lane >> 5;
@@ -117,12 +118,11 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     }
   }
   const Sees see = row_sees(A, s, r, group);
-  // this wave's tokens: some row sees them; every row sees those of full_lo .. full_hi
-  int wave_lo = 0, wave_hi = 0, full_lo = 0, full_hi = 0;
+  // every row of this wave sees the tokens from full_lo to full_hi
+  int full_lo = 0, full_hi = 0;
   if (wr0 < rows) {
     const int last = (wr0 + 32 < rows ? wr0 + 32 : rows) - 1;
-    const Sees a = row_sees(A, s, wr0, group), z = row_sees(A, s, last, group);
-    wave_lo = a.lo, wave_hi = z.hi, full_lo = z.lo, full_hi = a.hi;
+    full_lo = row_sees(A, s, last, group).lo, full_hi = row_sees(A, s, wr0, group).hi;
   }
 
   f32x16 o[ND];
@@ -132,157 +132,284 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   float m = -INFINITY, l = 0.0f, lref = P_LOG_MIN;
 
-  // a thread's pieces of the next tile
+  // A thread's pieces of the tiles to come.  The 64 pieces of a wave lie in one group of 16 tokens, for K
+  // and for V, so their page is one number a wave, read a tile ahead of the pieces, which thus never wait for
+  // the table, and the address is scalar work but for a lane's own offset, which does not change: with t a
+  // multiple of 64, place (t + j) % block is t % block + j % block.  Past the end the pieces are those of the
+  // last token's page: in bounds, of no use.
   u32x4v kp[PER], vp[PER];
-  float next_ks = 0.0f, next_vs = 0.0f, run_ref = P_LOG_MIN;
-  auto fetch = [&](int64_t t) {
+  int page_k[PER], page_v[PER], bad = 0;
+  const int wave0 = __builtin_amdgcn_readfirstlane((int)threadIdx.x) & ~63;
+  const int t0 = (int)first, t1 = (int)stop;
+  const uint32_t page_bytes = (uint32_t)A.cache.kv_heads * (uint32_t)(block * DIM);  // at most 2^31
+  const int8_t* k_base = A.cache.k_codes + (int64_t)hk * block * DIM;
+  const int8_t* v_base = A.cache.v_codes + (int64_t)hk * block * DIM;
+  // piece i of thread x (with more threads than pieces, two threads do the same one)
+  auto piece = [&](int x, int i) { return (x + i * NT) & (PIECES - 1); };
+  uint32_t off_k[PER], off_v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int p = piece(threadIdx.x, i);
+    off_k[i] = (uint32_t)((p / (DIM / 16) & (block - 1)) * DIM + p % (DIM / 16) * 16);
+    off_v[i] = (uint32_t)((16 * (p / DIM) & (block - 1)) * DIM + p % DIM * 16);
+  }
+  auto entry = [&](int tok) { return table[(tok < t1 ? tok : t1 - 1) >> shift]; };
+  auto checked = [&](int page) {
+    const bool ok = (uint32_t)page < (uint32_t)A.cache.pages;
+    bad |= !ok;
+    return ok ? (uint32_t)page : 0u;
+  };
+  auto pages = [&](int t_k, int t_v) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int p = threadIdx.x + i * NT;
-      if (PIECES % NT == 0 || p < PIECES) {
-        const int tok = p / (DIM / 16), c = p % (DIM / 16);
-        const int64_t sk = slot_at(A, table, t + (tok & ~15), stop, shift, hk);
-        kp[i] = *reinterpret_cast<const u32x4v*>(A.cache.k_codes +
-                                                 (sk * block + ((t + tok) & (block - 1))) * DIM + 16 * c);
-        const int g = p / DIM, d = p % DIM;
-        const int64_t sv = slot_at(A, table, t + 16 * g, stop, shift, hk);
-        vp[i] = *reinterpret_cast<const u32x4v*>(A.cache.v_codes + (sv * block + ((t + 16 * g) & (block - 1))) * DIM +
-                                                 16 * d);
-      }
-    }
-    if (threadIdx.x < 4) {
-      const int64_t sg = slot_at(A, table, t + 16 * threadIdx.x, stop, shift, hk);
-      next_ks = A.cache.k_scales[sg];
-      next_vs = t + 16 * threadIdx.x < stop ? A.cache.v_scales[sg] : 0.0f;
+      page_k[i] = entry(t_k + piece(wave0, i) / (DIM / 16));
+      page_v[i] = entry(t_v + 16 * (piece(wave0, i) / DIM));
     }
   };
-  auto place = [&](int buf) {
-    char* kb = lds + buf * KB;
-    char* vb = lds + 2 * KB + buf * VB;
+  auto fetch_k = [&](int t) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int p = threadIdx.x + i * NT;
-      if (PIECES % NT == 0 || p < PIECES) {
-        const int tok = p / (DIM / 16), c = p % (DIM / 16);
-        char* row = kb + tok * KROW;
-        *reinterpret_cast<f16x8*>(row + 16 * ((2 * c) ^ (tok & (KC - 1)))) = codes_to_f16(kp[i][0], kp[i][1]);
-        *reinterpret_cast<f16x8*>(row + 16 * ((2 * c + 1) ^ (tok & (KC - 1)))) = codes_to_f16(kp[i][2], kp[i][3]);
-        const int g = p / DIM, d = p % DIM;
-        row = vb + d * VROW;
-        *reinterpret_cast<f16x8*>(row + 16 * ((2 * g) ^ (d & 7))) = codes_to_f16(vp[i][0], vp[i][2]);
-        *reinterpret_cast<f16x8*>(row + 16 * ((2 * g + 1) ^ (d & 7))) = codes_to_f16(vp[i][1], vp[i][3]);
-      }
+      const uint32_t page = checked(__builtin_amdgcn_readfirstlane(page_k[i]));
+      kp[i] = *reinterpret_cast<const u32x4v*>(k_base + ((uint64_t)page * page_bytes + (uint32_t)((t & (block - 1)) * DIM)) +
+                                               off_k[i]);
     }
-    if (threadIdx.x < 4) {
-      const float lv = keep_nan_max(__log2f(next_vs), P_LOG_MIN);
-      float top = fmaxf(lv, P_LOG_MIN);
-      top = fmaxf(top, dpp<0xB1>(top));
-      top = fmaxf(top, dpp<0x4E>(top));
-      run_ref = fmaxf(run_ref, top);
-      const float lr = keep_nan_max(lv - run_ref, P_RATIO_MIN);
-      sc[buf].ks[threadIdx.x] = next_ks;
-      sc[buf].lr[threadIdx.x] = lr;
-      // with a scale of NaN the weights that see it are NaN; the sums of rows that do not are 0
-      sc[buf].ir[threadIdx.x] = lr != lr ? 1.0f : exp2_fast(-lr);
-      if (threadIdx.x == 0) sc[buf].lref = run_ref;
+  };
+  auto fetch_v = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t page = checked(__builtin_amdgcn_readfirstlane(page_v[i]));
+      vp[i] = *reinterpret_cast<const u32x4v*>(v_base + ((uint64_t)page * page_bytes + (uint32_t)((t & (block - 1)) * DIM)) +
+                                               off_v[i]);
+    }
+  };
+  // Quarter q of piece i, 8 codes widened and written: q 0, 1 of K's piece (tile tk), 2, 3 of V's (tile tv).
+  auto place = [&](int i, int q, int tk, int tv) {
+    const int p = piece(threadIdx.x, i);
+    if (q < 2) {
+      const int tok = p / (DIM / 16), c = 2 * (p % (DIM / 16)) + q;
+      *reinterpret_cast<f16x8*>(lds + (tk & 1) * KB + tok * KROW + 16 * (c ^ (tok & (KC - 1)))) =
+          codes_to_f16(kp[i][2 * q], kp[i][2 * q + 1]);
+    } else {
+      const int c = 2 * (p / DIM) + q - 2, d = p % DIM;
+      *reinterpret_cast<f16x8*>(lds + 2 * KB + (tv & 1) * VB + d * VROW + 16 * (c ^ (d >> 1 & 7))) =
+          codes_to_f16(vp[i][q - 2], vp[i][q]);
     }
   };
 
-  if (first < stop) {
-    fetch(first);
-    place(0);
-  }
-  __syncthreads();
-  int buf = 0;
-  for (int64_t t = first; t < stop; t += PT, buf ^= 1) {
-    const bool more = t + PT < stop;
-    if (more) fetch(t + PT);
-    if (t + PT > wave_lo && t < wave_hi) {
-      const char* kb = lds + buf * KB;
-      const char* vb = lds + 2 * KB + buf * VB;
-      f32x16 x[2];
+  // The scales of SB tiles at a time, by the first wave (lane 4 j + g: group g of the batch's tile j): pages
+  // looked up, scales read and the result placed in different turns, a batch ahead of its use.  The largest
+  // value scale so far is taken over the whole batch.
+  int page_s = 0;
+  float next_ks = 0.0f, next_vs = 0.0f, run_ref = P_LOG_MIN;
+  auto look_s = [&](int batch) { page_s = entry(t0 + PT * SB * batch + 16 * (lane & (4 * SB - 1))); };
+  auto fetch_s = [&](int batch) {
+    const bool ok = (uint32_t)page_s < (uint32_t)A.cache.pages;
+    if (!ok) bad = 1;
+    const int64_t sg = (int64_t)(ok ? page_s : 0) * A.cache.kv_heads + hk;
+    next_ks = A.cache.k_scales[sg];
+    next_vs = A.cache.v_scales[sg];
+    if (t0 + PT * SB * batch + 16 * (lane & (4 * SB - 1)) >= t1) next_vs = 0.0f;
+  };
+  auto place_s = [&](int batch) {
+    const float lv = keep_nan_max(__log2f(next_vs), P_LOG_MIN);
+    run_ref = fmaxf(run_ref, lv);
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
+    for (int k = 1; k < 4 * SB; k *= 2) run_ref = fmaxf(run_ref, __shfl_xor(run_ref, k));
+    const float lr = keep_nan_max(lv - run_ref, P_RATIO_MIN);
+    Scales& S = sc[SB * (batch & 1) + (lane >> 2 & (SB - 1))];
+    if (lane < 4 * SB) {
+      S.ks[lane & 3] = next_ks;
+      S.lr[lane & 3] = lr;
+      // with a scale of NaN the weights that see it are NaN; the sums of rows that do not are 0
+      S.ir[lane & 3] = lr != lr ? 1.0f : exp2_fast(-lr);
+      S.lref = run_ref;
+    }
+  };
+
+  f16x8 ph[4], pl[BF16 ? 1 : 4];  // a tile's weights, from its softmax to its output
+  auto softmax = [&]<bool MASKED>(int tile, f32x16 (&x)[2]) {
+    const Scales S = sc[tile & (2 * SB - 1)];
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = t0 + PT * tile + 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
+          x[tt][i] = j >= see.lo && j < see.hi ? x[tt][i] : -INFINITY;
+        }
+    }
+    float f[4], most = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      f[g] = S.ks[g] * qs;
+      float y = x[g >> 1][8 * (g & 1)];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) y = fmaxf(y, x[g >> 1][8 * (g & 1) + i]);
+      // a masked group stays out whatever its factor is (0, infinite or NaN)
+      most = fmaxf(most, MASKED && y == -INFINITY ? y : y * f[g]);
+    }
+    most = fmaxf(most, other_half(most));
+    const float mn = fmaxf(m, most);
+    if (__any(mn > m + P_SLACK || (m == -INFINITY && mn != m)) || S.lref != lref) {
+      const float base = mn == -INFINITY ? 0.0f : mn;
+      const float alpha = exp2_fast(m - base);
+      l *= alpha;
+      const float turn = alpha * exp2_fast(lref - S.lref);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] *= turn;
+      m = mn;
+      lref = S.lref;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float add = (P_EXP - base) + S.lr[g];
+      float p[8], sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = x[g >> 1][8 * (g & 1) + i];
+        float e = exp2_fast(fmaf(y, f[g], add));
+        if constexpr (MASKED) e = y == -INFINITY ? 0.0f : e;
+        p[i] = e;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += p[i];
+      if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ph[g][i] = (_Float16)p[i];
+      } else {
+        split16(p, ph[g], pl[g]);
+      }
+      l = fmaf(sum, S.ir[g], l);
+    }
+  };
+  // The matrix products of a turn: output of the tile before (PV), scores of this one (QK).  Their LDS operands
+  // are read AHEAD products before they are used, products that follow each other go to different accumulators,
+  // and the tiles to come are widened between them, 8 codes to two products (10 VALU instructions in the 64
+  // cycles of two): the order is written out here and kept.
+  auto products = [&]<bool PV, bool QK>(int tile, f32x16 (&x)[2]) {
+    constexpr int NPV = PV ? 4 * ND : 0, N = NPV + (QK ? 2 * NK : 0), AHEAD = 8;
+    constexpr int SIDES = QK ? 4 * PER + 2 : 0;
+    const char* vb = lds + 2 * KB + ((tile - 1) & 1) * VB;
+    const char* kb = lds + (tile & 1) * KB;
+    const int t = t0 + PT * tile;
+    auto operand = [&](int i) {
+      if (i < NPV) {
+        const int dd = 32 * (i % ND) + col;
+        return *reinterpret_cast<const f16x8*>(vb + dd * VROW + 16 * ((2 * (i / ND) + half) ^ (dd >> 1 & 7)));
+      }
+      const int k = (i - NPV) >> 1, tok = 32 * ((i - NPV) & 1) + col;
+      return *reinterpret_cast<const f16x8*>(kb + tok * KROW + 16 * ((2 * k + half) ^ (tok & (KC - 1))));
+    };
+    auto product = [&](int i, f16x8 a) {
+      if (i < NPV) {
+        const int g = i / ND, d = i % ND;
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, ph[g], o[d], 0, 0, 0);
+        if constexpr (!BF16) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, pl[g], o[d], 0, 0, 0);
+      } else {
+        const int k = (i - NPV) >> 1, tt = (i - NPV) & 1;
+        x[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qh[k], x[tt], 0, 0, 0);
+        if constexpr (!BF16) x[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, ql[k], x[tt], 0, 0, 0);
+      }
+    };
+    auto side = [&](int j) {
+      if (j < 4 * PER)
+        place(j / 4, j % 4, tile + 1, tile);
+      else if (j == 4 * PER) {
+        fetch_k(t + 2 * PT);
+        fetch_v(t + PT);
+      } else {
+        pages(t + 3 * PT, t + 2 * PT);
+      }
+    };
+    f16x8 a[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) a[i] = operand(i);
+    if constexpr (QK) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[tt][i] = 0.0f;
-        const int tok = 32 * tt + col;
-        const char* row = kb + tok * KROW;
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const f16x8 a = *reinterpret_cast<const f16x8*>(row + 16 * ((2 * k + half) ^ (tok & (KC - 1))));
-          x[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qh[k], x[tt], 0, 0, 0);
-          if constexpr (!BF16) x[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, ql[k], x[tt], 0, 0, 0);
-        }
+    for (int i = 0; i < N; i += 2) {
+      product(i, a[i % AHEAD]);
+      product(i + 1, a[(i + 1) % AHEAD]);
+      if (i + AHEAD < N) {
+        a[i % AHEAD] = operand(i + AHEAD);
+        a[(i + 1) % AHEAD] = operand(i + 1 + AHEAD);
       }
-      const Scales S = sc[buf];
-      const bool full = t >= full_lo && t + PT <= full_hi;
-      if (!full) {
+      if (i / 2 < SIDES) side(i / 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = (int)t + 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
-            x[tt][i] = j >= see.lo && j < see.hi ? x[tt][i] : -INFINITY;
-          }
-      }
-      float f[4], most = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        f[g] = S.ks[g] * qs;
-        float y = x[g >> 1][8 * (g & 1)];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) y = fmaxf(y, x[g >> 1][8 * (g & 1) + i]);
-        // a masked group stays out whatever its factor is (0, infinite or NaN)
-        most = fmaxf(most, y == -INFINITY ? y : y * f[g]);
-      }
-      most = fmaxf(most, other_half(most));
-      const float mn = fmaxf(m, most);
-      if (__any(mn > m + P_SLACK || (m == -INFINITY && mn != m)) || S.lref != lref) {
-        const float base = mn == -INFINITY ? 0.0f : mn;
-        const float alpha = exp2_fast(m - base);
-        l *= alpha;
-        const float turn = alpha * exp2_fast(lref - S.lref);
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[d] *= turn;
-        m = mn;
-        lref = S.lref;
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      f16x8 ph[4], pl[BF16 ? 1 : 4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float add = (P_EXP - base) + S.lr[g];
-        float p[8], sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = x[g >> 1][8 * (g & 1) + i];
-          float e = exp2_fast(fmaf(y, f[g], add));
-          if (!full) e = y == -INFINITY ? 0.0f : e;
-          p[i] = e;
-          sum += e;
-        }
-        l = fmaf(sum, S.ir[g], l);
-        if constexpr (BF16) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ph[g][i] = (_Float16)p[i];
-        } else {
-          split16(p, ph[g], pl[g]);
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const int dd = 32 * d + col;
-        const char* row = vb + dd * VROW;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f16x8 a = *reinterpret_cast<const f16x8*>(row + 16 * ((2 * g + half) ^ (dd & 7)));
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, ph[g], o[d], 0, 0, 0);
-          if constexpr (!BF16) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, pl[g], o[d], 0, 0, 0);
+    for (int j = N / 2; j < SIDES; ++j) side(j);
+    if constexpr (QK) {
+      if (wave == 0) {
+        const int batch = tile / SB + 1;
+        switch (tile & (SB - 1)) {
+          case 0: look_s(batch); break;
+          case 2: fetch_s(batch); break;
+          case 4: place_s(batch); break;
         }
       }
     }
-    if (more) place(buf ^ 1);
-    __syncthreads();
+  };
+  // Everything a wave has written to LDS is there for all when they pass; loads from HBM stay
+  // on their way.
+  auto meet = [&]() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  // A wave's turn i has two phases: matrix products (output of tile i - 1, scores of tile i) with the tiles to
+  // come brought in and widened beside them, then the softmax of tile i.  With 8 waves, two on a SIMD, the
+  // second four are a phase behind the first, so that one wave's products run beside the other's softmax.
+  // In slots (a slot ends where all meet) the first four have their products of turn i in slot 2 i, the
+  // second in slot 2 i + 1; in it a wave reads K(i) and V(i - 1) and writes its pieces of K(i + 1) and V(i).
+  // The buffers of K(i + 1) and V(i) held K(i - 1) and V(i - 2), last read in slot 2 i - 1, and are first read
+  // in slot 2 i + 2.
+  const int tiles = (t1 - t0 + PT - 1) / PT;
+  const bool late = wave >= 4;
+  if (tiles > 0) {
+    f32x16 x[2];
+    auto weigh = [&](int tile) {
+      const int t = t0 + PT * tile;
+      if (t >= full_lo && t + PT <= full_hi)
+        softmax.template operator()<false>(tile, x);
+      else
+        softmax.template operator()<true>(tile, x);
+    };
+    pages(t0, t0);
+    if (wave == 0) look_s(0);
+    fetch_k(t0);
+    fetch_v(t0);
+    pages(t0 + PT, t0);
+    if (wave == 0) fetch_s(0);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) place(i, 0, 0, 0), place(i, 1, 0, 0);
+    if (wave == 0) place_s(0);
+    fetch_k(t0 + PT);
+    pages(t0 + 2 * PT, t0 + PT);
+    meet();
+    if (late) meet();
+    products.template operator()<false, true>(0, x);
+    meet();
+    for (int tile = 0; tile < tiles - 1; ++tile) {
+      weigh(tile);
+      meet();
+      __builtin_amdgcn_s_setprio(1);
+      products.template operator()<true, true>(tile + 1, x);
+      __builtin_amdgcn_s_setprio(0);
+      meet();
+    }
+    weigh(tiles - 1);
+    meet();
+    products.template operator()<true, false>(tiles, x);
+    if (NW > 4 && !late) meet();
+    if (bad) raise_einval(A.d_status);
   }
 
   l += other_half(l);
