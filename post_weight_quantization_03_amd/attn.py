@@ -71,8 +71,11 @@ def bind(L):
 
 # --------------------------------------------------------------------------- helpers
 
-def _raw_stream(stream):
-    return _g._torch().cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+def _raw_stream(stream, like):
+    """The HIP stream of `stream`, or the current one of like's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _g._torch()._C._cuda_getCurrentRawStream(like.device.index)
 
 
 def _int32(name, t, shape=None):
@@ -112,7 +115,7 @@ def _weight(name, w, like):
 
 def _empty(shape, like, stream, dtype=None):
     """An output of the binding's own, tied to the stream that writes it."""
-    t = _g._torch().empty(shape, dtype=like.dtype if dtype is None else dtype, device=like.device)
+    t = like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -221,7 +224,7 @@ def gptq_qk_norm_rope(q, k, positions, rope: Rope, q_weight=None, k_weight=None,
         _int32("positions", positions, (tokens,))
     st = _g.lib().gptq_qk_norm_rope(cq, ck, _g._dtype_code(like), tokens, dim,
                                     None if positions is None else positions.data_ptr(), rope.c, _status(d_status),
-                                    _raw_stream(stream))
+                                    _raw_stream(stream, like))
     if st:
         raise _g.GptqError(st, "gptq_qk_norm_rope")
     return q_out, k_out
@@ -270,7 +273,7 @@ def gptq_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, rope: Rope, q_we
                                              None if positions is None else positions.data_ptr(), rope.c,
                                              None if workspace is None else workspace.data_ptr(),
                                              0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                             _status(d_status), _raw_stream(stream))
+                                             _status(d_status), _raw_stream(stream, like))
     if st:
         raise _g.GptqError(st, "gptq_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
@@ -286,7 +289,7 @@ def gptq_kv_append(cache: KVCache, batch: KVBatch, k, v, rope: Rope = None, k_we
     sk, sv = k.stride(), v.stride()
     st = _g.lib().gptq_kv_append(cache.c, batch.c, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1],
                                  _g._dtype_code(k), _weight("k_weight", k_weight, k),
-                                 None if rope is None else rope.c, _status(d_status), _raw_stream(stream))
+                                 None if rope is None else rope.c, _status(d_status), _raw_stream(stream, k))
     if st:
         raise _g.GptqError(st, "gptq_kv_append")
 
@@ -313,7 +316,7 @@ def gptq_kv_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=N
     like = k_out if k_out is not None else v_out
     st = _g.lib().gptq_kv_read(cache.c, batch.c, None if k_out is None else k_out.data_ptr(), sk[0], sk[1],
                                None if v_out is None else v_out.data_ptr(), sv[0], sv[1], _g._dtype_code(like),
-                               _status(d_status), _raw_stream(stream))
+                               _status(d_status), _raw_stream(stream, like))
     if st:
         raise _g.GptqError(st, "gptq_kv_read")
     return k_out, v_out
@@ -359,7 +362,7 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
                              None if lse is None else lse.data_ptr(), dt,
                              None if workspace is None else workspace.data_ptr(),
                              0 if workspace is None else workspace.numel() * workspace.element_size(),
-                             _status(d_status), _raw_stream(stream))
+                             _status(d_status), _raw_stream(stream, q))
     if st:
         raise _g.GptqError(st, "gptq_kv_attention")
     return out if lse is None else (out, lse)

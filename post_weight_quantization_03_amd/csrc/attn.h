@@ -72,7 +72,7 @@ struct KvAttention {
 size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool bf16,
                               const gptq_attention& a);
 // Whether the call's launches stay below 2^32 threads each.
-bool kv_attention_fits(const gptq_kv_cache& cache, const gptq_kv_batch& batch, const gptq_attention& a);
+bool kv_attention_fits(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool bf16, const gptq_attention& a);
 hipError_t kv_attention(const KvAttention& a, hipStream_t stream);
 
 inline bool kv_block_ok(int32_t block) { return block == 16 || block == 32 || block == 64 || block == 128; }

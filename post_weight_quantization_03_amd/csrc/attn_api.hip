@@ -253,7 +253,7 @@ int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, co
     return GPTQ_EINVAL;
   // with no token in any sequence no page exists to be pointed at
   if (batch->max_kv > 0 && (st = cache_pointers(cache)) != GPTQ_OK) return st;
-  if (!kv_attention_fits(*cache, *batch, *att)) return GPTQ_EUNSUPPORTED;
+  if (!kv_attention_fits(*cache, *batch, dtype == GPTQ_BF16, *att)) return GPTQ_EUNSUPPORTED;
   const size_t need = kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, *att);
   if (workspace_bytes < need || (need > 0 && !workspace)) return GPTQ_EWORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return GPTQ_EINVAL;

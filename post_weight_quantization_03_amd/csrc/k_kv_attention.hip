@@ -1,5 +1,6 @@
 // Attention over the paged 8-bit cache: which kernel takes a call, and how long
-// sequences are split.
+// sequences are split.  The host knows the sizes of a call but not its sequences'
+// lengths (max_kv bounds them), so the rules go by sizes.
 #include "kv_attend.h"
 
 namespace gptq {
@@ -10,47 +11,77 @@ struct Plan {
   int64_t chunk;
 };
 
-Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+// Rows (query tokens times heads of a key head's group) a workgroup takes.  Measured with groups of 4
+// over 4 x 30000, 16 x 2000 and 1 x 8000 tokens, 8 key heads (us, tiles of 16 / 32 / 128 / 256 rows):
+//   dim 128 bf16:   32 rows   83 / 93 / 121 / 191     32 / 31 / 52 / 83     18 / 18 / 22 / 25
+//                   64       149 / 112 / 128 / 196    47 / 46 / 61 / 93     23 / 25 / 25 / 28
+//                  128       284 / 198 / 120 / 175    86 / 64 / 51 / 60     32 / 31 / 27 / 31
+//                  200       474 / 419 / 222 / 187   132 / 117 / 76 / 77    54 / 54 / 34 / 34
+//   dim 128 fp32:   64       157 / 280 / 260 / 232    49 / 75 / 95 / 107    24 / 32 / 34 / 31
+//                  128       292 / 523 / 265 / 235    89 / 124 / 89 / 76    33 / 46 / 38 / 35
+//   dim 64 bf16:    64        88 / 68 / 97 / 183      29 / 31 / 50 / 82     16 / 17 / 19 / 23
+//                  800       821 / 822 / 386 / 471   224 / 226 / 117 / 155  83 / 82 / 57 / 69
+// fp32 keeps two parts of queries and weights in registers: its tiles of 32 rows and its 4 waves of 32
+// spill.  dim 256 fits 16 rows, or 4 waves of 32.
+int tile_rows_for(int64_t rows, int dim, bool bf16) {
+  if (dim == 256) return rows <= 64 ? 16 : 128;
+  if (rows <= 32) return 16;
+  if (dim == 128 && !bf16) return rows <= 64 ? 16 : 256;
+  if (rows <= 64) return 32;
+  return rows <= 128 || dim == 64 ? 128 : 256;
+}
+
+Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const gptq_attention& a) {
   const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
   Plan p;
-  if (rows <= 64)
-    p.tile_rows = rows > 16 && c.dim < 256 ? 32 : 16;
-  else
-    p.tile_rows = rows > 128 && c.dim < 256 ? 256 : 128;
-  const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  const int64_t base = b.batch * c.kv_heads * tiles;
+  p.tile_rows = tile_rows_for(rows, c.dim, bf16);
+  const int64_t base = b.batch * c.kv_heads * ((rows + p.tile_rows - 1) / p.tile_rows);
   // tokens a tile may see, with the rounding of its first
   int64_t span = b.max_kv;
   if (a.window > 0 && a.window + b.max_new < span) span = a.window + b.max_new;
   span += 63;
-  const int64_t want = (512 + base - 1) / base;
-  int64_t chunk = (span + want - 1) / want;
+  int64_t chunk;
+  if (p.tile_rows < 128) {
+    // Two workgroups of four waves a CU are resident: one round of 512 (one token over 131035 tokens, 8 key
+    // heads, chunks of 1024 / 2048 / 2304 / 4096: 60 / 56 / 60 / 88 us).  From 512 on no split is needed for
+    // the chip to be full (64 sequences of up to 8192, 32 heads: 475 us whole, 521 in two).
+    const int64_t want = (512 + base - 1) / base;
+    chunk = want == 1 ? span : (span / want + 128) / 256 * 256;
+  } else {
+    // One workgroup of eight waves a CU.  It starts and ends in the time of 5 tiles of 64 tokens, and its
+    // partial results cost a join, so one round of 256 does where chunks stay below 4096 tokens; above, up
+    // to three, which even out sequences of different lengths (500 tokens each over 6000 to 12001: 449 us
+    // whole, 382 in two, 350 in three, and 25 for the join).  From 448 on the later workgroups do that.
+    chunk = base >= 448 ? span : span * base / 256;
+    if (base < 448 && chunk > 4096) chunk = span * base / 768 > 4096 ? span * base / 768 : 4096;
+  }
   chunk = (chunk + 255) / 256 * 256;
-  p.chunk = chunk;
-  p.nsplit = (int)((span + chunk - 1) / chunk);
+  p.chunk = chunk < 256 ? 256 : chunk;
+  p.nsplit = (int)((span + p.chunk - 1) / p.chunk);
   return p;
 }
 
 }  // namespace
 
-size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool, const gptq_attention& a) {
-  const Plan p = make_plan(cache, batch, a);
+size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool bf16,
+                              const gptq_attention& a) {
+  const Plan p = make_plan(cache, batch, bf16, a);
   if (p.nsplit <= 1) return 0;
   return (size_t)batch.total * a.q_heads * p.nsplit * (cache.dim + 1) * sizeof(float);
 }
 
-bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const gptq_attention& a) {
   const int64_t limit = ((int64_t)1 << 32) - 1;
-  const Plan p = make_plan(c, b, a);
+  const Plan p = make_plan(c, b, bf16, a);
   // a workgroup a row and head where splits are joined
   if (p.nsplit > 1 && b.batch * b.max_new > limit / 256 / a.q_heads) return false;
   const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
   const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  return b.batch * c.kv_heads * tiles * p.nsplit <= limit / (p.tile_rows == 256 ? 512 : 256);
+  return b.batch * c.kv_heads * tiles <= limit / (p.tile_rows == 256 ? 512 : 256) / p.nsplit;
 }
 
 hipError_t kv_attention(const KvAttention& a, hipStream_t stream) {
-  const Plan p = make_plan(a.cache, a.batch, a.a);
+  const Plan p = make_plan(a.cache, a.batch, a.bf16, a.a);
   Partials w{nullptr, nullptr, p.nsplit, p.chunk};
   if (p.nsplit > 1) {
     w.out = static_cast<float*>(a.workspace);

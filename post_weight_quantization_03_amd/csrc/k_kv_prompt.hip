@@ -36,8 +36,17 @@ constexpr float P_RATIO_MIN = -60.0f; // log2 of its ratio to the largest, at le
 
 __device__ __forceinline__ float keep_nan_max(float x, float lo) { return x != x ? x : fmaxf(x, lo); }
 
-// the other half's value of the same column
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+// Maximum and sum over the two lanes of a column: v_permlane32_swap of x with itself leaves the lower
+// half's values in one register and the upper half's in the other (VALU; a shuffle would wait behind the
+// other waves' LDS reads).
+__device__ __forceinline__ float column_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float column_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 template <int DIM, bool BF16, int NW>
 __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAttention A, Partials P, uint32_t pairs,
@@ -60,11 +69,14 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 31, half = lane >> 5;
-  uint32_t id = blockIdx.x;
-  const uint32_t pair = id % pairs;  // workgroups of one sequence and key head: the same XCD where pairs is a multiple of 8
-  id /= pairs;
-  const int split = (int)(id % (uint32_t)P.nsplit);
-  const int rt = (int)(row_tiles - 1 - id / (uint32_t)P.nsplit);  // the longest of a causal call first
+  // Workgroups go to the XCDs in turn, and within one to its four shader engines in turn, waiting for the
+  // engine whose turn it is.  A sequence and key head (pair) stays on one XCD where pairs is a multiple of 8,
+  // and the pairs are shifted by 8 from one (row tile, split) to the next: else a long sequence's workgroups
+  // would all wait for one engine (a chunk of four prompts: 96 of 256 CUs busy at first).  The longest row
+  // tiles of a causal call come first.
+  const uint32_t rest = blockIdx.x / pairs, pair = (blockIdx.x + 8 * rest) % pairs;
+  const int split = (int)(rest % (uint32_t)P.nsplit);
+  const int rt = (int)(row_tiles - 1 - rest / (uint32_t)P.nsplit);
   const int hk = (int)(pair % (uint32_t)A.cache.kv_heads), b = (int)(pair / (uint32_t)A.cache.kv_heads);
   const Seq s = load_seq(A.batch, b, A.d_status);
   const int group = A.a.q_heads / A.cache.kv_heads;
@@ -100,7 +112,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[k][j]));
     }
-    most = fmaxf(most, other_half(most));
+    most = column_max(most);
     float up, down;
     row_scale(most, up, down);
     qs = fabsf(A.a.sm_scale) * 1.44269504088896340736f * down;
@@ -227,8 +239,8 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   };
 
   f16x8 ph[4], pl[BF16 ? 1 : 4];  // a tile's weights, from its softmax to its output
+  Scales S;                       // its scales, read with the last operands of its scores
   auto softmax = [&]<bool MASKED>(int tile, f32x16 (&x)[2]) {
-    const Scales S = sc[tile & (2 * SB - 1)];
     if constexpr (MASKED) {
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
@@ -242,13 +254,14 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       f[g] = S.ks[g] * qs;
-      float y = x[g >> 1][8 * (g & 1)];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) y = fmaxf(y, x[g >> 1][8 * (g & 1) + i]);
+      const int e = 8 * (g & 1);
+      const f32x16& z = x[g >> 1];
+      const float y = fmaxf(fmaxf(fmaxf(fmaxf(z[e], z[e + 1]), z[e + 2]), fmaxf(fmaxf(z[e + 3], z[e + 4]), z[e + 5])),
+                            fmaxf(z[e + 6], z[e + 7]));
       // a masked group stays out whatever its factor is (0, infinite or NaN)
       most = fmaxf(most, MASKED && y == -INFINITY ? y : y * f[g]);
     }
-    most = fmaxf(most, other_half(most));
+    most = column_max(most);
     const float mn = fmaxf(m, most);
     if (__any(mn > m + P_SLACK || (m == -INFINITY && mn != m)) || S.lref != lref) {
       const float base = mn == -INFINITY ? 0.0f : mn;
@@ -341,6 +354,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
         a[(i + 1) % AHEAD] = operand(i + 1 + AHEAD);
       }
       if (i / 2 < SIDES) side(i / 2);
+      if (QK && i + 4 == N) S = sc[tile & (2 * SB - 1)];
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -412,7 +426,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     if (bad) raise_einval(A.d_status);
   }
 
-  l += other_half(l);
+  l = column_sum(l);
   if (r >= rows) return;
   const float inv = l == 0.0f ? 0.0f : exp2_fast(lref) / l;
   const float lse2 = l == 0.0f ? -INFINITY : m + __log2f(l) - P_EXP;
@@ -465,21 +479,15 @@ hipError_t launch(const KvAttention& a, const Partials& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int DIM>
-hipError_t launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
-  if constexpr (DIM < 256) {
-    if (tile_rows == 256) return a.bf16 ? launch<DIM, true, 8>(a, p, stream) : launch<DIM, false, 8>(a, p, stream);
-  }
-  return a.bf16 ? launch<DIM, true, 4>(a, p, stream) : launch<DIM, false, 4>(a, p, stream);
-}
-
 }  // namespace
 
 hipError_t kv_prompt_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
   switch (a.cache.dim) {
-    case 64: return launch<64>(a, p, tile_rows, stream);
-    case 128: return launch<128>(a, p, tile_rows, stream);
-    default: return launch<256>(a, p, tile_rows, stream);
+    case 64: return a.bf16 ? launch<64, true, 4>(a, p, stream) : launch<64, false, 4>(a, p, stream);
+    case 128:
+      if (!a.bf16) return launch<128, false, 8>(a, p, stream);
+      return tile_rows == 256 ? launch<128, true, 8>(a, p, stream) : launch<128, true, 4>(a, p, stream);
+    default: return a.bf16 ? launch<256, true, 4>(a, p, stream) : launch<256, false, 4>(a, p, stream);
   }
 }
 

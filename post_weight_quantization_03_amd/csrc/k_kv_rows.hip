@@ -41,9 +41,11 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n16 = lane & 15, g = lane >> 4;
-  uint32_t id = blockIdx.x;
-  const int split = (int)(id % (uint32_t)P.nsplit);
-  id /= (uint32_t)P.nsplit;
+  // The splits are the slowest index: workgroups go to the XCDs and their shader engines in turn, and the
+  // last splits, which short sequences lack, would else leave some of these idle.
+  const uint32_t tiles = (uint32_t)A.batch.batch * (uint32_t)A.cache.kv_heads * row_tiles;
+  const int split = (int)(blockIdx.x / tiles);
+  uint32_t id = blockIdx.x % tiles;
   const int rt = (int)(id % row_tiles);
   id /= row_tiles;
   const int hk = (int)(id % (uint32_t)A.cache.kv_heads), b = (int)(id / (uint32_t)A.cache.kv_heads);
@@ -59,6 +61,39 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   const int32_t* table = A.batch.block_table + b * A.batch.table_stride;
   const int shift = __builtin_ctz((unsigned)A.cache.block);
   const int block = A.cache.block;
+
+  // the first tile is on its way while the queries are read and scaled
+  u32x4v kr[4][NI], vr[ND];
+  float ks = 0.0f, vs = 0.0f;
+  auto slots = [&](int64_t t, int64_t& sk, int64_t& sv) {
+    sk = slot_at(A, table, t + 16 * (n16 >> 2), stop, shift, hk);
+    sv = slot_at(A, table, t + 16 * g, stop, shift, hk);
+  };
+  auto load_k = [&](int64_t t, int64_t sk, int64_t sv) {
+    const int off = (int)((t + 16 * (n16 >> 2)) & (block - 1)) + (n16 & 3);
+    const int8_t* p = A.cache.k_codes + (sk * block + off) * DIM + 16 * g;
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) kr[tt][i] = *reinterpret_cast<const u32x4v*>(p + 4 * tt * DIM + 64 * i);
+    ks = A.cache.k_scales[sv];
+  };
+  auto load_v = [&](int64_t t, int64_t sv) {
+    const int off = (int)((t + 16 * g) & (block - 1));
+    const int8_t* p = A.cache.v_codes + (sv * block + off) * DIM + 16 * n16;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) vr[d] = *reinterpret_cast<const u32x4v*>(p + 256 * d);
+    vs = A.cache.v_scales[sv];
+  };
+
+  int64_t t = first + 64 * wave;
+  int64_t sk = 0, sv = 0, sk1 = 0, sv1 = 0;
+  if (t < stop) {
+    slots(t, sk, sv);
+    load_k(t, sk, sv);
+    load_v(t, sv);
+    if (t + 64 * KW < stop) slots(t + 64 * KW, sk1, sv1);
+  }
 
   // queries, scaled to [2^7, 2^8) by row
   f16x8 qh[CT][NK], ql[CT][BF16 ? 1 : NK];
@@ -120,37 +155,6 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
     for (int d = 0; d < ND; ++d) o[c][d] = (f32x4){0, 0, 0, 0};
   }
 
-  u32x4v kr[4][NI], vr[ND];
-  float ks = 0.0f, vs = 0.0f;
-  auto slots = [&](int64_t t, int64_t& sk, int64_t& sv) {
-    sk = slot_at(A, table, t + 16 * (n16 >> 2), stop, shift, hk);
-    sv = slot_at(A, table, t + 16 * g, stop, shift, hk);
-  };
-  auto load_k = [&](int64_t t, int64_t sk, int64_t sv) {
-    const int off = (int)((t + 16 * (n16 >> 2)) & (block - 1)) + (n16 & 3);
-    const int8_t* p = A.cache.k_codes + (sk * block + off) * DIM + 16 * g;
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) kr[tt][i] = *reinterpret_cast<const u32x4v*>(p + 4 * tt * DIM + 64 * i);
-    ks = A.cache.k_scales[sv];
-  };
-  auto load_v = [&](int64_t t, int64_t sv) {
-    const int off = (int)((t + 16 * g) & (block - 1));
-    const int8_t* p = A.cache.v_codes + (sv * block + off) * DIM + 16 * n16;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) vr[d] = *reinterpret_cast<const u32x4v*>(p + 256 * d);
-    vs = A.cache.v_scales[sv];
-  };
-
-  int64_t t = first + 64 * wave;
-  int64_t sk = 0, sv = 0, sk1 = 0, sv1 = 0;
-  if (t < stop) {
-    slots(t, sk, sv);
-    load_k(t, sk, sv);
-    load_v(t, sv);
-    if (t + 64 * KW < stop) slots(t + 64 * KW, sk1, sv1);
-  }
   for (; t < stop; t += 64 * KW) {
     const int64_t tn = t + 64 * KW;
     // scores
@@ -389,7 +393,7 @@ hipError_t launch(const KvAttention& a, const Partials& p, int tile_rows, hipStr
   const int64_t rows = a.batch.max_new * (a.a.q_heads / a.cache.kv_heads);
   const uint32_t tiles = (uint32_t)((rows + tile_rows - 1) / tile_rows);
   const uint32_t grid = (uint32_t)(a.batch.batch * a.cache.kv_heads * tiles * p.nsplit);
-  if constexpr (DIM < 256) {
+  if constexpr (DIM == 64 || (DIM == 128 && BF16)) {
     if (tile_rows == 32)
       k_kv_rows<DIM, BF16, 2><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
     else

@@ -109,11 +109,11 @@ struct Partials {
   int64_t chunk;
 };
 
-// k_kv_rows.hip: row tiles of 16 or 32 (dim 256: 16).
+// k_kv_rows.hip: row tiles of 16, or of 32 for dim 64 and for bf16 of dim 128.
 hipError_t kv_rows_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream);
 // Joins the splits (k_kv_rows.hip).
 hipError_t kv_join_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream);
-// k_kv_prompt.hip: row tiles of 128 or 256 (dim 256: 128).
+// k_kv_prompt.hip: row tiles of 128, or of 256 for dim 128 (always for fp32 of dim 128).
 hipError_t kv_prompt_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream);
 
 }  // namespace gptq
