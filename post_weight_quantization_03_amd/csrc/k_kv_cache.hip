@@ -35,11 +35,15 @@ __device__ __forceinline__ float needed_scale(uint32_t m) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ int to_code(float x) {
-  return (int)rintf(fminf(fmaxf(x, -127.0f), 127.0f));  // a NaN gives a number too
-}
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+// Four codes from elements and the factor 1 / scale: x * factor + 1.5 * 2^23 is rounded to an integer, ties to
+// even, whose two's complement is the number's low byte (|x * factor| <= 127; otherwise the scale is NaN and
+// the codes are of no use).
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float factor) {
+  const float magic = 12582912.0f;
+  const uint32_t x = __float_as_uint(fmaf(a, factor, magic)), y = __float_as_uint(fmaf(b, factor, magic));
+  const uint32_t z = __float_as_uint(fmaf(c, factor, magic)), w = __float_as_uint(fmaf(d, factor, magic));
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w, z, 0x0c0c0400u), __builtin_amdgcn_perm(y, x, 0x0c0c0400u),
+                               0x05040100u);
 }
 __device__ __forceinline__ int byte_of(uint32_t w, int i) { return (int)(w << (24 - 8 * i)) >> 24; }
 
@@ -47,8 +51,7 @@ __device__ __forceinline__ u32x4v rescaled(u32x4v w, float ratio) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t x = w[i];
-    w[i] = pack4(to_code((float)byte_of(x, 0) * ratio), to_code((float)byte_of(x, 1) * ratio),
-                 to_code((float)byte_of(x, 2) * ratio), to_code((float)byte_of(x, 3) * ratio));
+    w[i] = codes4((float)byte_of(x, 0), (float)byte_of(x, 1), (float)byte_of(x, 2), (float)byte_of(x, 3), ratio);
   }
   return w;
 }
@@ -76,24 +79,19 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvAppend A, uint32_t n
   const int blk = before / block + j;
   const int64_t start = (int64_t)blk * block;
   if (start >= s.len) return;
-  const int64_t page = A.batch.block_table[b * A.batch.table_stride + blk];
   const int lo = (int)((before > start ? before : start) - start);
   const int hi = (int)((s.len < start + block ? s.len : start + block) - start);
-  if (page < 0 || page >= A.cache.pages || (!is_v && A.rope.rot > 0 && start + hi > A.rope.max_pos)) {
-    raise_einval(A.d_status);
-    return;
-  }
-  const int64_t slot = page * A.cache.kv_heads + h;
-  int8_t* codes = (is_v ? A.cache.v_codes : A.cache.k_codes) + slot * block * dim;
-  float* scale_at = (is_v ? A.cache.v_scales : A.cache.k_scales) + slot;
-  const float was = *scale_at;
-
+  const int64_t page = A.batch.block_table[b * A.batch.table_stride + blk];  // on its way beside the elements
   const int L = dim / 16;
   const int l = threadIdx.x & (L - 1), group = threadIdx.x / L, groups = KV_THREADS / L;
   const Runs u = is_v ? Runs{16 * l, 16 * l + 8, -1} : head_runs(l, A.rope.rot, A.rope.interleaved);
   const void* src = is_v ? A.v : A.k;
   const int64_t st = is_v ? A.v_token : A.k_token, sh = is_v ? A.v_head : A.k_head;
+  // cos and sin come with the elements where registers allow, else when they are needed
+  constexpr bool EARLY = IT <= 1;
+  const bool turned = u.pair >= 0 && start + hi <= A.rope.max_pos;
   float xa[IT][8], xb[IT][8];
+  Turn turn[EARLY ? IT : 1];
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
     const int tok = it * groups + group;
@@ -103,8 +101,17 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvAppend A, uint32_t n
       const int64_t o = (s.row + (start + tok - before)) * st + h * sh;
       load8<BF16, VEC>(src, o + u.a, xa[it]);
       load8<BF16, VEC>(src, o + u.b, xb[it]);
+      if (EARLY && turned) load_turn(A.rope, start + tok, u.pair, turn[it]);
     }
   }
+  if (page < 0 || page >= A.cache.pages || (!is_v && A.rope.rot > 0 && start + hi > A.rope.max_pos)) {
+    raise_einval(A.d_status);
+    return;
+  }
+  const int64_t slot = page * A.cache.kv_heads + h;
+  int8_t* codes = (is_v ? A.cache.v_codes : A.cache.k_codes) + slot * block * dim;
+  float* scale_at = (is_v ? A.cache.v_scales : A.cache.k_scales) + slot;
+  const float was = lo > 0 ? *scale_at : 0.0f;  // only a block that holds tokens has one
   if (!is_v) {
     if (A.k_weight) {
       float wa[8], wb[8];
@@ -125,14 +132,13 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvAppend A, uint32_t n
         }
       }
     }
-    if (u.pair >= 0) {
+    if (turned) {
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
         const int tok = it * groups + group;
         if (tok >= lo && tok < hi) {
-          Turn turn;
-          load_turn(A.rope, start + tok, u.pair, turn);
-          turn16(xa[it], xb[it], turn, A.rope.interleaved, false);
+          if (!EARLY) load_turn(A.rope, start + tok, u.pair, turn[0]);
+          turn16(xa[it], xb[it], turn[EARLY ? it : 0], A.rope.interleaved, false);
         }
       }
     }
@@ -142,9 +148,8 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvAppend A, uint32_t n
 #pragma unroll
   for (int it = 0; it < IT; ++it)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m = max(m, __float_as_uint(xa[it][i]) & 0x7fffffffu);
-      m = max(m, __float_as_uint(xb[it][i]) & 0x7fffffffu);
+    for (int i = 0; i < 8; ++i) {  // the bits without the sign
+      m = max(m, max(__float_as_uint(xa[it][i]) << 1, __float_as_uint(xb[it][i]) << 1));
     }
 #pragma unroll
   for (int k = 1; k < 64; k *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, k));
@@ -152,7 +157,7 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvAppend A, uint32_t n
   __syncthreads();
   m = max(max(wave_max[0], wave_max[1]), max(wave_max[2], wave_max[3]));
 
-  const float need = needed_scale(m);
+  const float need = needed_scale(m >> 1);
   const bool carried = lo > 0;
   const float scale = !carried ? need : was != was ? was : need <= was ? was : need;
   const bool grown = carried && scale > was;
@@ -163,14 +168,10 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvAppend A, uint32_t n
   for (int it = 0; it < IT; ++it) {
     const int tok = it * groups + group;
     if (tok < lo || tok >= hi) continue;
-    const u32x2v a = {pack4(to_code(xa[it][0] * inv), to_code(xa[it][1] * inv), to_code(xa[it][2] * inv),
-                            to_code(xa[it][3] * inv)),
-                      pack4(to_code(xa[it][4] * inv), to_code(xa[it][5] * inv), to_code(xa[it][6] * inv),
-                            to_code(xa[it][7] * inv))};
-    const u32x2v c = {pack4(to_code(xb[it][0] * inv), to_code(xb[it][1] * inv), to_code(xb[it][2] * inv),
-                            to_code(xb[it][3] * inv)),
-                      pack4(to_code(xb[it][4] * inv), to_code(xb[it][5] * inv), to_code(xb[it][6] * inv),
-                            to_code(xb[it][7] * inv))};
+    const u32x2v a = {codes4(xa[it][0], xa[it][1], xa[it][2], xa[it][3], inv),
+                      codes4(xa[it][4], xa[it][5], xa[it][6], xa[it][7], inv)};
+    const u32x2v c = {codes4(xb[it][0], xb[it][1], xb[it][2], xb[it][3], inv),
+                      codes4(xb[it][4], xb[it][5], xb[it][6], xb[it][7], inv)};
     int8_t* dst = (is_v ? staged : codes) + tok * dim;
     *reinterpret_cast<u32x2v*>(dst + u.a) = a;
     *reinterpret_cast<u32x2v*>(dst + u.b) = c;
@@ -185,25 +186,44 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvAppend A, uint32_t n
     return;
   }
   __syncthreads();
-  const int g0 = grown ? 0 : lo / 16, g1 = (hi + 15) / 16;
-  for (int i = g0 * dim + threadIdx.x; i < g1 * dim; i += KV_THREADS) {
-    const int g = i / dim, d = i - g * dim;  // piece i: tokens 16 g .. 16 g + 15 of element d
-    u32x4v* p = reinterpret_cast<u32x4v*>(codes) + i;
-    u32x4v w = {0, 0, 0, 0};
-    if (16 * g < lo) {
-      w = *p;
-      if (grown) w = rescaled(w, ratio);
-    }
+  // A thread takes 16 tokens of 4 neighbouring elements: 16 dwords of LDS, transposed byte by byte (4 x 4
+  // at a time, 8 v_perm) into the four pieces.
+  const int g0 = grown ? 0 : lo / 16, g1 = (hi + 15) / 16, quads = dim / 4;
+  for (int i = g0 * quads + threadIdx.x; i < g1 * quads; i += KV_THREADS) {
+    const int g = i / quads, d = 4 * (i - g * quads);
+    u32x4v* p = reinterpret_cast<u32x4v*>(codes + (g * dim + d) * 16);
+    u32x4v w[4];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int tok = 16 * g + k;
-      const uint32_t mask = 255u << (8 * (k & 3));
-      if (tok >= lo) {
-        const uint32_t c = tok < hi ? (uint8_t)staged[tok * dim + d] : 0u;
-        w[k >> 2] = (w[k >> 2] & ~mask) | c << (8 * (k & 3));
+    for (int k = 0; k < 4; ++k) {
+      uint32_t r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int tok = 16 * g + 4 * k + j;
+        r[j] = tok >= lo && tok < hi ? *reinterpret_cast<const uint32_t*>(staged + tok * dim + d) : 0u;
+      }
+      const uint32_t a = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), c = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
+      const uint32_t e = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u), f = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+      w[0][k] = __builtin_amdgcn_perm(e, a, 0x05040100u);
+      w[1][k] = __builtin_amdgcn_perm(e, a, 0x07060302u);
+      w[2][k] = __builtin_amdgcn_perm(f, c, 0x05040100u);
+      w[3][k] = __builtin_amdgcn_perm(f, c, 0x07060302u);
+    }
+    if (16 * g < lo) {  // the piece holds old tokens too
+      const int old = lo - 16 * g < 16 ? lo - 16 * g : 16;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u32x4v x = p[j];
+        if (grown) x = rescaled(x, ratio);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int n = old - 4 * k;
+          const uint32_t mask = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1;
+          w[j][k] = (x[k] & mask) | (w[j][k] & ~mask);
+        }
       }
     }
-    *p = w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = w[j];
   }
 }
 

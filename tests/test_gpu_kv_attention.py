@@ -60,6 +60,7 @@ FORMS = [
     ([500, 131], [131, 131], 6, 2, 64, 128),          # chunks over earlier tokens, 393 rows
     ([300], [100], 4, 2, 256, 32),
     ([129, 40], [129, 0], 2, 1, 128, 16),             # a sequence without new tokens
+    ([600, 257], [300, 257], 3, 1, 128, 128),         # 900 rows of one key head
 ]
 
 
@@ -78,7 +79,8 @@ def test_against_reference(form, bf16, mask):
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("form", [([5000, 40, 1300], [1, 1, 1], 4, 2, 128, 64), ([3000], [2], 8, 8, 64, 16),
                                   ([2100, 10], [40, 10], 4, 1, 128, 32), ([1600], [4], 2, 1, 256, 128),
-                                  ([2500, 90], [70, 70], 4, 2, 64, 128)])
+                                  ([2500, 90], [70, 70], 4, 2, 64, 128), ([3000, 700], [150, 20], 4, 2, 128, 64),
+                                  ([900, 5000, 140], [130, 90, 140], 2, 2, 128, 16)])
 def test_split_sequences(form, bf16):
     """Lengths that are split over workgroups and joined, with short ones in the same call."""
     lengths, new, qh, kh, dim, block = form
