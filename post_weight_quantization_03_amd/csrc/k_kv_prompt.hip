@@ -24,6 +24,9 @@
 // sum are rescaled only when a row's maximum has grown by more than 2^8.
 #include "kv_attend.h"
 
+// The kernel's parts are lambdas over its registers: a call left in place would put those in memory.
+#define INLINE __attribute__((always_inline))
+
 namespace gptq {
 namespace {
 
@@ -91,11 +94,14 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   const int shift = __builtin_ctz((unsigned)A.cache.block);
   const int block = A.cache.block;
 
-  // queries
+  // Queries, scaled to [2^7, 2^8) by row; the tokens a row sees, and those from full_lo to full_hi that every
+  // row of this wave sees.
   const int wr0 = r0 + 32 * wave, r = wr0 + col;
   f16x8 qh[NK], ql[BF16 ? 1 : NK];
-  float qs;
-  {
+  float qs = 0.0f;
+  Sees see = {0, 0};
+  int full_lo = 0, full_hi = 0;
+  auto load_queries = [&]() INLINE {
     float x[NK][8];
     float most = 0.0f;
 #pragma unroll
@@ -128,14 +134,12 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
         split16(x[k], qh[k], ql[k]);
       }
     }
-  }
-  const Sees see = row_sees(A, s, r, group);
-  // every row of this wave sees the tokens from full_lo to full_hi
-  int full_lo = 0, full_hi = 0;
-  if (wr0 < rows) {
-    const int last = (wr0 + 32 < rows ? wr0 + 32 : rows) - 1;
-    full_lo = row_sees(A, s, last, group).lo, full_hi = row_sees(A, s, wr0, group).hi;
-  }
+    see = row_sees(A, s, r, group);
+    if (wr0 < rows) {
+      const int last = (wr0 + 32 < rows ? wr0 + 32 : rows) - 1;
+      full_lo = row_sees(A, s, last, group).lo, full_hi = row_sees(A, s, wr0, group).hi;
+    }
+  };
 
   f32x16 o[ND];
 #pragma unroll
@@ -157,7 +161,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   const int8_t* k_base = A.cache.k_codes + (int64_t)hk * block * DIM;
   const int8_t* v_base = A.cache.v_codes + (int64_t)hk * block * DIM;
   // piece i of thread x (with more threads than pieces, two threads do the same one)
-  auto piece = [&](int x, int i) { return (x + i * NT) & (PIECES - 1); };
+  auto piece = [&](int x, int i) INLINE { return (x + i * NT) & (PIECES - 1); };
   uint32_t off_k[PER], off_v[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -165,20 +169,20 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     off_k[i] = (uint32_t)((p / (DIM / 16) & (block - 1)) * DIM + p % (DIM / 16) * 16);
     off_v[i] = (uint32_t)((16 * (p / DIM) & (block - 1)) * DIM + p % DIM * 16);
   }
-  auto entry = [&](int tok) { return table[(tok < t1 ? tok : t1 - 1) >> shift]; };
-  auto checked = [&](int page) {
+  auto entry = [&](int tok) INLINE { return table[(tok < t1 ? tok : t1 - 1) >> shift]; };
+  auto checked = [&](int page) INLINE {
     const bool ok = (uint32_t)page < (uint32_t)A.cache.pages;
     bad |= !ok;
     return ok ? (uint32_t)page : 0u;
   };
-  auto pages = [&](int t_k, int t_v) {
+  auto pages = [&](int t_k, int t_v) INLINE {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       page_k[i] = entry(t_k + piece(wave0, i) / (DIM / 16));
       page_v[i] = entry(t_v + 16 * (piece(wave0, i) / DIM));
     }
   };
-  auto fetch_k = [&](int t) {
+  auto fetch_k = [&](int t) INLINE {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const uint32_t page = checked(__builtin_amdgcn_readfirstlane(page_k[i]));
@@ -186,7 +190,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
                                                off_k[i]);
     }
   };
-  auto fetch_v = [&](int t) {
+  auto fetch_v = [&](int t) INLINE {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const uint32_t page = checked(__builtin_amdgcn_readfirstlane(page_v[i]));
@@ -194,16 +198,16 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
                                                off_v[i]);
     }
   };
-  // Quarter q of piece i, 8 codes widened and written: q 0, 1 of K's piece (tile tk), 2, 3 of V's (tile tv).
-  auto place = [&](int i, int q, int tk, int tv) {
+  // Quarter q of piece i, 8 codes widened and written: q 0, 1 of K's piece (to buffer bk), 2, 3 of V's (bv).
+  auto place = [&](int i, int q, int bk, int bv) INLINE {
     const int p = piece(threadIdx.x, i);
     if (q < 2) {
       const int tok = p / (DIM / 16), c = 2 * (p % (DIM / 16)) + q;
-      *reinterpret_cast<f16x8*>(lds + (tk & 1) * KB + tok * KROW + 16 * (c ^ (tok & (KC - 1)))) =
+      *reinterpret_cast<f16x8*>(lds + bk * KB + tok * KROW + 16 * (c ^ (tok & (KC - 1)))) =
           codes_to_f16(kp[i][2 * q], kp[i][2 * q + 1]);
     } else {
       const int c = 2 * (p / DIM) + q - 2, d = p % DIM;
-      *reinterpret_cast<f16x8*>(lds + 2 * KB + (tv & 1) * VB + d * VROW + 16 * (c ^ (d >> 1 & 7))) =
+      *reinterpret_cast<f16x8*>(lds + 2 * KB + bv * VB + d * VROW + 16 * (c ^ (d >> 1 & 7))) =
           codes_to_f16(vp[i][q - 2], vp[i][q]);
     }
   };
@@ -213,8 +217,8 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   // value scale so far is taken over the whole batch.
   int page_s = 0;
   float next_ks = 0.0f, next_vs = 0.0f, run_ref = P_LOG_MIN;
-  auto look_s = [&](int batch) { page_s = entry(t0 + PT * SB * batch + 16 * (lane & (4 * SB - 1))); };
-  auto fetch_s = [&](int batch) {
+  auto look_s = [&](int batch) INLINE { page_s = entry(t0 + PT * SB * batch + 16 * (lane & (4 * SB - 1))); };
+  auto fetch_s = [&](int batch) INLINE {
     const bool ok = (uint32_t)page_s < (uint32_t)A.cache.pages;
     if (!ok) bad = 1;
     const int64_t sg = (int64_t)(ok ? page_s : 0) * A.cache.kv_heads + hk;
@@ -222,7 +226,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     next_vs = A.cache.v_scales[sg];
     if (t0 + PT * SB * batch + 16 * (lane & (4 * SB - 1)) >= t1) next_vs = 0.0f;
   };
-  auto place_s = [&](int batch) {
+  auto place_s = [&](int batch) INLINE {
     const float lv = keep_nan_max(__log2f(next_vs), P_LOG_MIN);
     run_ref = fmaxf(run_ref, lv);
 #pragma unroll
@@ -240,7 +244,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
 
   f16x8 ph[4], pl[BF16 ? 1 : 4];  // a tile's weights, from its softmax to its output
   Scales S;                       // its scales, read with the last operands of its scores
-  auto softmax = [&]<bool MASKED>(int tile, f32x16 (&x)[2]) {
+  auto softmax = [&]<bool MASKED>(int tile, f32x16 (&x)[2]) INLINE {
     if constexpr (MASKED) {
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
@@ -300,13 +304,13 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   // are read AHEAD products before they are used, products that follow each other go to different accumulators,
   // and the tiles to come are widened between them, 8 codes to two products (10 VALU instructions in the 64
   // cycles of two): the order is written out here and kept.
-  auto products = [&]<bool PV, bool QK>(int tile, f32x16 (&x)[2]) {
+  auto products = [&]<bool PV, bool QK>(int tile, f32x16 (&x)[2]) INLINE {
     constexpr int NPV = PV ? 4 * ND : 0, N = NPV + (QK ? 2 * NK : 0), AHEAD = 8;
     constexpr int SIDES = QK ? 4 * PER + 2 : 0;
     const char* vb = lds + 2 * KB + ((tile - 1) & 1) * VB;
     const char* kb = lds + (tile & 1) * KB;
     const int t = t0 + PT * tile;
-    auto operand = [&](int i) {
+    auto operand = [&](int i) INLINE {
       if (i < NPV) {
         const int dd = 32 * (i % ND) + col;
         return *reinterpret_cast<const f16x8*>(vb + dd * VROW + 16 * ((2 * (i / ND) + half) ^ (dd >> 1 & 7)));
@@ -314,7 +318,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
       const int k = (i - NPV) >> 1, tok = 32 * ((i - NPV) & 1) + col;
       return *reinterpret_cast<const f16x8*>(kb + tok * KROW + 16 * ((2 * k + half) ^ (tok & (KC - 1))));
     };
-    auto product = [&](int i, f16x8 a) {
+    auto product = [&](int i, f16x8 a) INLINE {
       if (i < NPV) {
         const int g = i / ND, d = i % ND;
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, ph[g], o[d], 0, 0, 0);
@@ -325,9 +329,9 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
         if constexpr (!BF16) x[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, ql[k], x[tt], 0, 0, 0);
       }
     };
-    auto side = [&](int j) {
+    auto side = [&](int j) INLINE {
       if (j < 4 * PER)
-        place(j / 4, j % 4, tile + 1, tile);
+        place(j / 4, j % 4, (tile + 1) & 1, tile & 1);
       else if (j == 4 * PER) {
         fetch_k(t + 2 * PT);
         fetch_v(t + PT);
@@ -372,7 +376,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   };
   // Everything a wave has written to LDS is there for all when they pass; loads from HBM stay
   // on their way.
-  auto meet = [&]() {
+  auto meet = [&]() INLINE {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -389,7 +393,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   const bool late = wave >= 4;
   if (tiles > 0) {
     f32x16 x[2];
-    auto weigh = [&](int tile) {
+    auto weigh = [&](int tile) INLINE {
       const int t = t0 + PT * tile;
       if (t >= full_lo && t + PT <= full_hi)
         softmax.template operator()<false>(tile, x);
@@ -402,6 +406,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     fetch_v(t0);
     pages(t0 + PT, t0);
     if (wave == 0) fetch_s(0);
+    load_queries();  // while the first tile is on its way
 #pragma unroll
     for (int i = 0; i < PER; ++i) place(i, 0, 0, 0), place(i, 1, 0, 0);
     if (wave == 0) place_s(0);
