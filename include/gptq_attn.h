@@ -101,7 +101,8 @@ int gptq_qk_norm_rope_backward(const gptq_heads_grad* q, const gptq_heads_grad* 
  *           side by side: the order in which the matrix cores take them)
  *   k_scales, v_scales fp32 [pages][kv_heads]
  * block 16, 32, 64 or 128; dim 64, 128 or 256 (else GPTQ_EUNSUPPORTED).
- * Code pointers 16-byte aligned.  Nothing has to be cleared before first use. */
+ * Code pointers 16-byte aligned.  Nothing has to be cleared before first use.
+ * Scales are not negative; gptq_kv_append writes powers of two, or NaN. */
 typedef struct {
   int8_t* k_codes;
   int8_t* v_codes;
@@ -168,7 +169,7 @@ int gptq_kv_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch, void* k
  *   lse     fp32 [total, q_heads], contiguous; NULL: not written
  * Products run on the matrix cores with fp32 accumulation.  Codes are exact in
  * fp16.  A bf16 query, scaled by a power of two of its row, is exact in fp16 as
- * far as 2^-22 of the row's largest element; weights are rounded to fp16 (2^-12)
+ * far as 2^-22 of the row's largest element; weights are rounded to fp16 (2^-11)
  * before the second product.  For fp32, query and weights go in two fp16 parts
  * each (about 2^-22).  Maximum, sum and output are kept in fp32.  Results are
  * bit-reproducible run to run.

@@ -201,15 +201,6 @@ __device__ __forceinline__ float head_sum(float x, int L) {
   if (L > 16) x += __shfl_xor(x, 16);
   return x;
 }
-__device__ __forceinline__ float head_max(float x, int L) {
-  if (L > 1) x = fmaxf(x, dpp<0xB1>(x));
-  if (L > 2) x = fmaxf(x, dpp<0x4E>(x));
-  if (L > 4) x = fmaxf(x, dpp<0x141>(x));
-  if (L > 8) x = fmaxf(x, dpp<0x140>(x));
-  if (L > 16) x = fmaxf(x, __shfl_xor(x, 16));
-  return x;
-}
-
 __device__ __forceinline__ void raise_einval(int32_t* st) {
   if (st) atomicMax(st, (int)GPTQ_EINVAL);
 }

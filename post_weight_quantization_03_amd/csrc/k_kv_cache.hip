@@ -14,8 +14,13 @@
 // integer maximum of the bits (in which anything not finite exceeds all
 // numbers), fixes the scale and writes codes.  Values go through LDS to their
 // 16-tokens-of-one-d order and out in 16-byte pieces; a piece that holds old
-// tokens is read, merged and written, by the one thread that owns it.  Bound by
-// HBM for prompts, by latency for single tokens.
+// tokens is read, merged and written, by the one thread that owns it.
+//
+// Three prompts of 8608 tokens in all, 32 heads of 128, bf16 with norm and rotation: 211 MB in 61 to 67 us,
+// 3.2 to 3.5 TB/s of the 4.9 of a copy; the many short-lived workgroups (12672 of 16 KB) bound it, not
+// VALU work or occupancy, and longer-lived ones that take 8 heads in turn are slower (75 us).  One token of
+// each of 64 sequences, 8 heads: 7 us, five dependent accesses.  Reading 214 MB of them back takes 35 us,
+// 6.1 TB/s.
 #include "attn.h"
 
 namespace gptq {

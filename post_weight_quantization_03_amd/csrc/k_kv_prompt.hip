@@ -3,25 +3,35 @@
 // S^T = K Q^T and O^T += V^T P^T on v_mfma_f32_32x32x16_f16.  A wave keeps 32 rows
 // (query token and head of one key head's group) as the columns: queries and
 // output in registers, keys and values of 64 tokens in LDS, shared by the
-// workgroup's waves.  Codes are widened to fp16 once, on their way into LDS (a
-// thread loads 16 of them while the tile before is worked on), because widening
-// them in every wave would cost as many VALU cycles as the softmax.
+// workgroup's waves.  Codes are widened to fp16 once, on their way into LDS;
+// widening them in every wave would cost as many VALU cycles as the softmax.
 //
 // Column q of S^T lies in lanes q and q + 32, which hold tokens 8 (r / 4) + 4 half +
 // r % 4; the values' 16 tokens are stored in LDS in the order (0-3, 8-11, 4-7,
 // 12-15), so that a lane's weights are its operand of the second product where
-// they are.  LDS rows are XOR-swizzled in 16-byte pieces; reads and writes are
-// 16-byte and conflict-free.
+// they are.  LDS rows are XOR-swizzled in 16-byte pieces for 64 banks (swizzled
+// for 32, reads of V took twice the cycles).
 //
-// What bounds it: per wave and tile the two products take 1024 cycles (dim 128),
-// the softmax about as many VALU cycles (32 exponentials a lane at a quarter of
-// the rate are half of it), and the LDS reads of the CU's 8 waves 2048 at 128 bytes
-// a cycle against 2048 of a SIMD's two waves of products.  The softmax is therefore
-// kept to an fma, an exponential and an addition a score: the key scale times the
-// row's constant is one factor, the maximum is taken before it (it is not
+// What bounds it (dim 128, 256 rows, 64 tokens a turn): per wave and turn 32
+// products of 32 cycles and some 190 VALU instructions of the softmax, 34 of them
+// exponentials at a quarter of the rate, and 70 of the widening.  Run one after the
+// other these took 7000 cycles a turn of the SIMD's two waves.  So the two waves
+// of a SIMD run half a turn apart, one's products beside the other's softmax, with a
+// barrier where they change over, LDS operands are read 8 products ahead in an order
+// that is written out, and addresses, page look-ups and the scales of 8 tiles at a
+// time stay out of the softmax: 4300 cycles.  What is left is the issue of VALU and
+// matrix instructions, which share a SIMD's port (a product holds it for its operand
+// reads), and the power limit: sustained, the clock is near 2.0 GHz.  A causal prompt of
+// 4096 tokens and 32 heads takes 164 to 180 us, 760 to 840 TFLOP/s of the products that it
+// needs, 0.62 to 0.69 of a large library product's rate; starting and ending a workgroup
+// costs 11 us each, a tenth of it.
+//
+// The softmax is an fma, an exponential and an addition a score: the key scale
+// times the row's constant is one factor, the maximum is taken before it (it is not
 // negative), the value scale is added to the exponent (log2 of its ratio to the
 // largest so far) and taken back out of the sum once for 16 tokens, and output and
-// sum are rescaled only when a row's maximum has grown by more than 2^8.
+// sum are rescaled only when a row's maximum has grown by more than 2^8.  Sums are of
+// the unrounded weights (of the rounded ones, two at a time, lse lost 1e-4).
 #include "kv_attend.h"
 
 // The kernel's parts are lambdas over its registers: a call left in place would put those in memory.

@@ -19,6 +19,11 @@
 // and output; they are joined in LDS at the end, and over the splits of a long
 // sequence by k_kv_join.
 //
+// One token over 64 sequences of 2048 to 8192 tokens, 32 heads of 128: 2.69 GB in 467 us, 5.76 TB/s (a large
+// copy moves 4.9 TB/s, read and written); over 131035 tokens, 8 key heads: 268 MB in 55 us, and 5 for
+// joining 64 splits; over 43 tokens 7.4 us, the latencies of lengths, table, cache and output in turn.
+// Three waves a SIMD instead of two spill: 707 us for the first.
+//
 // Scales: K's multiplies the score.  V's enters the weight as its ratio to the
 // largest seen so far (like the running maximum), so fp16 weights keep their range
 // whatever the scales are.

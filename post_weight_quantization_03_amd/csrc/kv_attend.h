@@ -7,7 +7,6 @@ namespace gptq {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Weights enter the second product as 2^KV_PEXP e^(s - m) <= 2^KV_PEXP in fp16:

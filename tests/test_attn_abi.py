@@ -5,6 +5,7 @@ every call below returns from its host-side checks."""
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -195,3 +196,13 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         attn.KVBatch(torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                      torch.zeros((2, 4), dtype=torch.int32), 2, 1, 4)
+
+
+def test_header_is_plain_c(tmp_path):
+    src = tmp_path / "user.c"
+    src.write_text('#include "gptq_attn.h"\nint main(void) { gptq_kv_cache c = {0}; gptq_kv_batch b = {0};\n'
+                   '  gptq_attention a = {32, 0.1f, 1, 0};\n'
+                   '  return (int)gptq_kv_attention_workspace_bytes(&c, &b, GPTQ_BF16, &a); }\n')
+    r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-fsyntax-only", "-I",
+                        os.path.dirname(HEADER), str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
