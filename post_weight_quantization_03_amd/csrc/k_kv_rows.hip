@@ -67,37 +67,50 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   const int shift = __builtin_ctz((unsigned)A.cache.block);
   const int block = A.cache.block;
 
-  // the first tile is on its way while the queries are read and scaled
+  // A lane's K rows of a tile lie in group n16 / 4 of its four groups of 16 tokens, its V pieces and its scores'
+  // scales in group g.  The pages of both are read a tile ahead of what they hold and looked at only then (a
+  // wait for the table would wait for the loads before it, too).  Past the end they are the last token's.
   u32x4v kr[4][NI], vr[ND];
   float ks = 0.0f, vs = 0.0f;
-  auto slots = [&](int64_t t, int64_t& sk, int64_t& sv) {
-    sk = slot_at(A, table, t + 16 * (n16 >> 2), stop, shift, hk);
-    sv = slot_at(A, table, t + 16 * g, stop, shift, hk);
+  int page_k = 0, page_v = 0, bad = 0;
+  const int gk = n16 >> 2;
+  const uint32_t page_bytes = (uint32_t)A.cache.kv_heads * (uint32_t)(block * DIM);  // at most 2^31
+  const int8_t* k_base = A.cache.k_codes + (int64_t)hk * block * DIM + (n16 & 3) * DIM + 16 * g;
+  const int8_t* v_base = A.cache.v_codes + (int64_t)hk * block * DIM + 16 * n16;
+  const int t_stop = (int)stop;
+  auto pages = [&](int t) {
+    const int tk = t + 16 * gk, tv = t + 16 * g;
+    page_k = table[(tk < t_stop ? tk : t_stop - 1) >> shift];
+    page_v = table[(tv < t_stop ? tv : t_stop - 1) >> shift];
   };
-  auto load_k = [&](int64_t t, int64_t sk, int64_t sv) {
-    const int off = (int)((t + 16 * (n16 >> 2)) & (block - 1)) + (n16 & 3);
-    const int8_t* p = A.cache.k_codes + (sk * block + off) * DIM + 16 * g;
+  auto checked = [&](int page) {
+    const bool ok = (uint32_t)page < (uint32_t)A.cache.pages;
+    bad |= !ok;
+    return ok ? (uint32_t)page : 0u;
+  };
+  auto load_k = [&](int t) {
+    const int8_t* p = k_base + (uint64_t)checked(page_k) * page_bytes + (uint32_t)(((t + 16 * gk) & (block - 1)) * DIM);
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
       for (int i = 0; i < NI; ++i) kr[tt][i] = *reinterpret_cast<const u32x4v*>(p + 4 * tt * DIM + 64 * i);
-    ks = A.cache.k_scales[sv];
+    ks = A.cache.k_scales[(int64_t)checked(page_v) * A.cache.kv_heads + hk];
   };
-  auto load_v = [&](int64_t t, int64_t sv) {
-    const int off = (int)((t + 16 * g) & (block - 1));
-    const int8_t* p = A.cache.v_codes + (sv * block + off) * DIM + 16 * n16;
+  auto load_v = [&](int t) {
+    const uint32_t page = checked(page_v);
+    const int8_t* p = v_base + (uint64_t)page * page_bytes + (uint32_t)(((t + 16 * g) & (block - 1)) * DIM);
 #pragma unroll
     for (int d = 0; d < ND; ++d) vr[d] = *reinterpret_cast<const u32x4v*>(p + 256 * d);
-    vs = A.cache.v_scales[sv];
+    vs = A.cache.v_scales[(int64_t)page * A.cache.kv_heads + hk];
   };
 
-  int64_t t = first + 64 * wave;
-  int64_t sk = 0, sv = 0, sk1 = 0, sv1 = 0;
-  if (t < stop) {
-    slots(t, sk, sv);
-    load_k(t, sk, sv);
-    load_v(t, sv);
-    if (t + 64 * KW < stop) slots(t + 64 * KW, sk1, sv1);
+  // the first tile is on its way while the queries are read and scaled
+  int t = (int)first + 64 * wave;
+  if (t < t_stop) {
+    pages(t);
+    load_k(t);
+    load_v(t);
+    pages(t + 64 * KW);
   }
 
   // queries, scaled to [2^7, 2^8) by row
@@ -160,8 +173,8 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
     for (int d = 0; d < ND; ++d) o[c][d] = (f32x4){0, 0, 0, 0};
   }
 
-  for (; t < stop; t += 64 * KW) {
-    const int64_t tn = t + 64 * KW;
+  for (; t < t_stop; t += 64 * KW) {
+    const int tn = t + 64 * KW;
     // scores
     f32x4 x[CT][4];
 #pragma unroll
@@ -180,8 +193,8 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
       }
     }
     const float ks_now = ks;
-    float vs_now = t + 16 * g < stop ? vs : 0.0f;
-    if (tn < stop) load_k(tn, sk1, sv1);
+    const float vs_now = t + 16 * g < t_stop ? vs : 0.0f;
+    if (tn < t_stop) load_k(tn);
 
     // V's scales against the largest seen so far
     float rt_max = fmaxf(vs_now, __shfl_xor(vs_now, 16));
@@ -203,7 +216,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
         for (int r = 0; r < 4; ++r) {
           float y = x[c][tt][r] * f;
           if (!full) {
-            const int j = (int)t + 16 * g + 4 * tt + r;
+            const int j = t + 16 * g + 4 * tt + r;
             y = j >= see[c].lo && j < see[c].hi ? y : -INFINITY;
           }
           x[c][tt][r] = y;
@@ -257,12 +270,12 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
           if constexpr (!BF16) o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[c][u], o[c][d], 0, 0, 0);
         }
       }
-    if (tn < stop) {
-      load_v(tn, sv1);
-      sk = sk1, sv = sv1;
-      if (tn + 64 * KW < stop) slots(tn + 64 * KW, sk1, sv1);
+    if (tn < t_stop) {
+      load_v(tn);
+      pages(tn + 64 * KW);
     }
   }
+  if (bad) raise_einval(A.d_status);
 
   // join the waves
 #pragma unroll

@@ -84,21 +84,6 @@ __device__ __forceinline__ void row_scale(float most, float& up, float& down) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Slot (page and key head) of the 16 tokens from `tok` on; slot of page 0, raised,
-// where the table's entry is out of range, and silently past `end`.
-__device__ __forceinline__ int64_t slot_at(const KvAttention& A, const int32_t* table, int64_t tok, int64_t end,
-                                           int shift, int hk) {
-  int64_t page = 0;
-  if (tok < end) {
-    page = table[tok >> shift];
-    if (page < 0 || page >= A.cache.pages) {
-      raise_einval(A.d_status);
-      page = 0;
-    }
-  }
-  return page * A.cache.kv_heads + hk;
-}
-
 // Partial results of split sequences: per row and head, `nsplit` rows of dim fp32
 // (normalised) and their log2 sums.
 struct Partials {
