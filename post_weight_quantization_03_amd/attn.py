@@ -96,29 +96,40 @@ def _status(t):
 
 
 def _heads(name, t, dtype=None, shape=None):
-    """Checks a [tokens, heads, dim] tensor with unit stride in dim; any strides before it."""
-    if t.dim() != 3 or not t.is_cuda or t.stride(2) != 1 and t.shape[2] > 1:
+    """Checks a [tokens, heads, dim] tensor with unit stride in dim, any strides before it, and returns its strides."""
+    s = t.stride()
+    if len(s) != 3 or not t.is_cuda or s[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name} must be a [tokens, heads, dim] device tensor with unit stride in dim")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return s
 
 
 def _weight(name, w, like):
     if w is None:
         return None
-    if w.dtype != like.dtype or w.shape != like.shape[2:] or not w.is_cuda or not w.is_contiguous():
+    if w.dtype != like.dtype or w.dim() != 1 or w.numel() != like.shape[2] or not w.is_cuda or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [dim] device tensor of dtype {like.dtype}")
     return w.data_ptr()
 
 
-def _empty(shape, like, stream, dtype=None):
-    """An output of the binding's own, tied to the stream that writes it."""
-    t = like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+def _kept(t, stream):
+    """Ties an output of the binding's own to the stream that writes it."""
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _empty(shape, like, stream, dtype):
+    return _kept(like.new_empty(shape, dtype=dtype), stream)
+
+
+def _empty_as(like, stream, dtype=None):
+    """A contiguous tensor of like's shape."""
+    torch = _g._torch()
+    return _kept(torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format), stream)
 
 
 # --------------------------------------------------------------------------- handles
@@ -197,12 +208,12 @@ def _check_plan(cache, batch):
 def _side(name, x, weight, out, stream):
     if x is None:
         return None, None
-    _heads(name, x)
+    sx = _heads(name, x)
     if out is None:
-        out = _empty(x.shape, x, stream)
+        out = _empty_as(x, stream)
+        sy = out.stride()
     else:
-        _heads(name + "_out", out, x.dtype, x.shape)
-    sx, sy = x.stride(), out.stride()
+        sy = _heads(name + "_out", out, x.dtype, x.shape)
     return out, gptq_heads(x.data_ptr(), sx[0], sx[1], out.data_ptr(), sy[0], sy[1],
                            _weight(name + "_weight", weight, x), x.shape[1])
 
@@ -237,16 +248,16 @@ def gptq_qk_norm_rope_backward_workspace_bytes(tokens: int, dim: int, q_heads: i
 def _grad_side(name, dy, x, weight, stream):
     if dy is None:
         return None, None, None
-    _heads("d" + name, dy)
+    sg = _heads("d" + name, dy)
+    sx = (0, 0)
     if weight is not None:
         if x is None:
             raise ValueError(f"{name} is needed with its weight")
-        _heads(name, x, dy.dtype, dy.shape)
-    dx = _empty(dy.shape, dy, stream)
-    dw = None if weight is None else _empty(weight.shape, weight, stream, _g._torch().float32)
-    sg, sd = dy.stride(), dx.stride()
-    sx = x.stride() if x is not None else (0, 0)
-    return dx, dw, gptq_heads_grad(dy.data_ptr(), sg[0], sg[1], None if x is None else x.data_ptr(), sx[0], sx[1],
+        sx = _heads(name, x, dy.dtype, dy.shape)
+    dx = _empty_as(dy, stream)
+    dw = None if weight is None else _empty_as(weight, stream, _g._torch().float32)
+    sd = dx.stride()
+    return dx, dw, gptq_heads_grad(dy.data_ptr(), sg[0], sg[1], None if weight is None else x.data_ptr(), sx[0], sx[1],
                                    dx.data_ptr(), sd[0], sd[1], _weight(name + "_weight", weight, dy),
                                    None if dw is None else dw.data_ptr(), dy.shape[1])
 
@@ -284,9 +295,8 @@ def gptq_kv_append(cache: KVCache, batch: KVBatch, k, v, rope: Rope = None, k_we
     """Stores the batch's new tokens: k, v [total, kv_heads, dim] (bf16 or fp32), k through the norm
     (k_weight) and rotation (rope) at its place in the sequence."""
     _check_plan(cache, batch)
-    _heads("k", k, None, (batch.total, cache.kv_heads, cache.dim))
-    _heads("v", v, k.dtype, k.shape)
-    sk, sv = k.stride(), v.stride()
+    sk = _heads("k", k, None, (batch.total, cache.kv_heads, cache.dim))
+    sv = _heads("v", v, k.dtype, k.shape)
     st = _g.lib().gptq_kv_append(cache.c, batch.c, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1],
                                  _g._dtype_code(k), _weight("k_weight", k_weight, k),
                                  None if rope is None else rope.c, _status(d_status), _raw_stream(stream, k))
@@ -308,11 +318,9 @@ def gptq_kv_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=N
         v_out = _empty(shape, cache.k_codes, stream, dtype)
     sk = sv = (0, 0)
     if k_out is not None:
-        _heads("k_out", k_out, dtype, shape)
-        sk = k_out.stride()
+        sk = _heads("k_out", k_out, dtype, shape)
     if v_out is not None:
-        _heads("v_out", v_out, dtype, shape)
-        sv = v_out.stride()
+        sv = _heads("v_out", v_out, dtype, shape)
     like = k_out if k_out is not None else v_out
     st = _g.lib().gptq_kv_read(cache.c, batch.c, None if k_out is None else k_out.data_ptr(), sk[0], sk[1],
                                None if v_out is None else v_out.data_ptr(), sv[0], sv[1], _g._dtype_code(like),
@@ -336,14 +344,15 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
     is given or wanted.  Rows that no sequence owns are left as they are."""
     _check_plan(cache, batch)
     torch = _g._torch()
-    _heads("q", q)
+    sq = _heads("q", q)
     total, heads, dim = q.shape
     if total != batch.total or dim != cache.dim:
         raise ValueError("shape mismatch")
     if out is None:
-        out = _empty(q.shape, q, stream)
+        out = _empty_as(q, stream)
+        so = out.stride()
     else:
-        _heads("out", out, q.dtype, q.shape)
+        so = _heads("out", out, q.dtype, q.shape)
     if lse is None:
         if want_lse:
             lse = _empty((total, heads), q, stream, torch.float32)
@@ -357,7 +366,6 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
         need = L.gptq_kv_attention_workspace_bytes(cache.c, batch.c, dt, a)
         if need:
             workspace = _g._workspace(need, q, stream)
-    sq, so = q.stride(), out.stride()
     st = L.gptq_kv_attention(cache.c, batch.c, a, q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0], so[1],
                              None if lse is None else lse.data_ptr(), dt,
                              None if workspace is None else workspace.data_ptr(),
