@@ -232,10 +232,18 @@ static int attention_check(const gptq_kv_cache* cache, const gptq_kv_batch* batc
   return GPTQ_OK;
 }
 
+// A window that no sequence outgrows is no window (places are below max_kv); what is left of it stays below
+// 2^30, so sums with it fit.
+static gptq_attention limited(const gptq_attention* a, const gptq_kv_batch* batch) {
+  gptq_attention r = *a;
+  if (r.window >= batch->max_kv) r.window = 0;
+  return r;
+}
+
 size_t gptq_kv_attention_workspace_bytes(const gptq_kv_cache* cache, const gptq_kv_batch* batch, gptq_dtype dtype,
                                          const gptq_attention* a) {
   if (attention_check(cache, batch, dtype, a) != GPTQ_OK || batch_empty(batch)) return 0;
-  return kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, *a);
+  return kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, limited(a, batch));
 }
 
 int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const gptq_attention* att, const void* q,
@@ -253,14 +261,15 @@ int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, co
     return GPTQ_EINVAL;
   // with no token in any sequence no page exists to be pointed at
   if (batch->max_kv > 0 && (st = cache_pointers(cache)) != GPTQ_OK) return st;
-  if (!kv_attention_fits(*cache, *batch, dtype == GPTQ_BF16, *att)) return GPTQ_EUNSUPPORTED;
-  const size_t need = kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, *att);
+  const gptq_attention seen = limited(att, batch);
+  if (!kv_attention_fits(*cache, *batch, dtype == GPTQ_BF16, seen)) return GPTQ_EUNSUPPORTED;
+  const size_t need = kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, seen);
   if (workspace_bytes < need || (need > 0 && !workspace)) return GPTQ_EWORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return GPTQ_EINVAL;
   KvAttention a{};
   a.cache = *cache;
   a.batch = *batch;
-  a.a = *att;
+  a.a = seen;
   a.q = q, a.q_token = q_token, a.q_head = q_head;
   a.out = out, a.out_token = out_token, a.out_head = out_head;
   a.lse = lse;

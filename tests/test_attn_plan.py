@@ -1,0 +1,35 @@
+"""The attention operators' plans on the host (no GPU): workspace sizes and refusals at the ends of
+the arguments' ranges.  Pointers passed here are never dereferenced."""
+
+import pytest
+
+import post_weight_quantization_03_amd as g
+from post_weight_quantization_03_amd import attn
+
+A = 0x1000  # an aligned address that is not used
+
+
+def cache(kv_heads=8, block=64, dim=128, pages=1 << 20):
+    return attn.gptq_kv_cache(A, A, A, A, pages, kv_heads, block, dim)
+
+
+def batch(n=1, total=1, max_new=1, max_kv=131035, block=64):
+    return attn.gptq_kv_batch(A, A, A, -(-max_kv // block), n, total, max_new, max_kv)
+
+
+def workspace(c, b, q_heads=32, dtype=0, causal=1, window=0):
+    return int(g.lib().gptq_kv_attention_workspace_bytes(c, b, dtype, attn.gptq_attention(q_heads, 0.1, causal, window)))
+
+
+SIZES = [dict(), dict(n=4, total=2000, max_new=500, max_kv=12001), dict(total=4096, max_new=4096, max_kv=4096),
+         dict(n=2, total=80, max_new=40, max_kv=3000)]
+
+
+@pytest.mark.parametrize("sizes", SIZES)
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("causal", [0, 1])
+def test_a_window_as_long_as_the_sequences_is_no_window(sizes, dtype, causal):
+    """The workspace holds the splits of what is seen: every window from max_kv on sees all."""
+    want = workspace(cache(), batch(**sizes), dtype=dtype, causal=causal)
+    for window in (batch(**sizes).max_kv, 1 << 31, 1 << 62, (1 << 63) - 1 - batch(**sizes).max_new, (1 << 63) - 1):
+        assert workspace(cache(), batch(**sizes), dtype=dtype, causal=causal, window=window) == want
