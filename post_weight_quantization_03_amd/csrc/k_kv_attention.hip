@@ -8,8 +8,11 @@ namespace {
 
 struct Plan {
   int tile_rows, nsplit;
-  int64_t chunk;
+  int64_t chunk, base;  // base: workgroups without splits
 };
+
+// a * b, or the largest number where that is larger (a, b >= 0): sizes each in range can have a product past 64 bits.
+int64_t product(int64_t a, int64_t b) { return a != 0 && b > INT64_MAX / a ? INT64_MAX : a * b; }
 
 // Rows (query tokens times heads of a key head's group) a workgroup takes.  Measured with groups of 4
 // over 4 x 30000, 16 x 2000 and 1 x 8000 tokens, 8 key heads (us, tiles of 16 / 32 / 128 / 256 rows):
@@ -35,7 +38,8 @@ Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const 
   const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
   Plan p;
   p.tile_rows = tile_rows_for(rows, c.dim, bf16);
-  const int64_t base = b.batch * c.kv_heads * ((rows + p.tile_rows - 1) / p.tile_rows);
+  const int64_t base = product(b.batch * c.kv_heads, (rows + p.tile_rows - 1) / p.tile_rows);
+  p.base = base;
   // tokens a tile may see, with the rounding of its first
   int64_t span = b.max_kv;
   if (a.window > 0 && a.window + b.max_new < span) span = a.window + b.max_new;
@@ -45,7 +49,7 @@ Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const 
     // Two workgroups of four waves a CU are resident: one round of 512 (one token over 131035 tokens, 8 key
     // heads, chunks of 1024 / 2048 / 2304 / 4096: 60 / 56 / 60 / 88 us).  From 512 on no split is needed for
     // the chip to be full (64 sequences of up to 8192, 32 heads: 475 us whole, 521 in two).
-    const int64_t want = (512 + base - 1) / base;
+    const int64_t want = base >= 512 ? 1 : (512 + base - 1) / base;
     chunk = want == 1 ? span : (span / want + 128) / 256 * 256;
   } else {
     // One workgroup of eight waves a CU.  It starts and ends in the time of 5 tiles of 64 tokens, and its
@@ -67,6 +71,7 @@ size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& b
                               const gptq_attention& a) {
   const Plan p = make_plan(cache, batch, bf16, a);
   if (p.nsplit <= 1) return 0;
+  // at most 768 workgroups' splits of 256 rows, times 2^30 tokens: below 2^60
   return (size_t)batch.total * a.q_heads * p.nsplit * (cache.dim + 1) * sizeof(float);
 }
 
@@ -75,9 +80,7 @@ bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16
   const Plan p = make_plan(c, b, bf16, a);
   // a workgroup a row and head where splits are joined
   if (p.nsplit > 1 && b.batch * b.max_new > limit / 256 / a.q_heads) return false;
-  const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
-  const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  return b.batch * c.kv_heads * tiles <= limit / (p.tile_rows == 256 ? 512 : 256) / p.nsplit;
+  return p.base <= limit / (p.tile_rows == 256 ? 512 : 256) / p.nsplit;
 }
 
 hipError_t kv_attention(const KvAttention& a, hipStream_t stream) {

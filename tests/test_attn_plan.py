@@ -33,3 +33,22 @@ def test_a_window_as_long_as_the_sequences_is_no_window(sizes, dtype, causal):
     want = workspace(cache(), batch(**sizes), dtype=dtype, causal=causal)
     for window in (batch(**sizes).max_kv, 1 << 31, 1 << 62, (1 << 63) - 1 - batch(**sizes).max_new, (1 << 63) - 1):
         assert workspace(cache(), batch(**sizes), dtype=dtype, causal=causal, window=window) == want
+
+
+def attend(c, b, q_heads, ws_bytes=(1 << 64) - 1):
+    return g.lib().gptq_kv_attention(c, b, attn.gptq_attention(q_heads, 0.1, 1, 0), A, 128, 128, 2 * A, 128, 128, None,
+                                     0, A, ws_bytes, None, None)
+
+
+BIG = 1 << 30
+
+
+@pytest.mark.parametrize("n,max_new,q_heads,kv_heads,max_kv", [
+    (BIG, BIG, 65536, 1, 64),            # 2^68 workgroups: 0 in 64 bits
+    (BIG, BIG, 65536, 65536, 64),
+    ((1 << 29) + 1, BIG, 65536, 1, 64),
+    (BIG, BIG, 65536, 1, 1 << 20),       # the same with splits
+    (BIG, BIG - 256, 49152, 1, 64),
+])
+def test_calls_past_what_a_launch_holds_are_refused(n, max_new, q_heads, kv_heads, max_kv):
+    assert attend(cache(kv_heads), batch(n, BIG, max_new, max_kv), q_heads) == g.GPTQ_EUNSUPPORTED
