@@ -61,10 +61,11 @@ typedef struct {
 } gptq_heads;
 
 /* q->y and k->y as above for `tokens` tokens; positions int32 [tokens], each in
- * [0, max_pos).  x, y and weight are all of type dtype (bf16 or fp32).  y may
- * be x with the same strides; otherwise they must not overlap.  dim: a multiple
- * of 16, at most 512.  Vectors of 16 bytes are used where pointers and strides
- * allow, single elements otherwise.  tokens == 0 or no heads: no work. */
+ * [0, max_pos) (max_pos 0 with tokens to rotate: GPTQ_EINVAL).  x, y and weight
+ * are all of type dtype (bf16 or fp32).  y may be x with the same strides;
+ * otherwise they must not overlap.  dim: a multiple of 16, at most 512.  Vectors
+ * of 16 bytes are used where pointers and strides allow, single elements
+ * otherwise.  tokens == 0 or no heads: no work. */
 int gptq_qk_norm_rope(const gptq_heads* q, const gptq_heads* k, gptq_dtype dtype, int64_t tokens, int32_t dim,
                       const int32_t* positions, const gptq_rope* rope, int32_t* d_status, gptq_stream_t stream);
 

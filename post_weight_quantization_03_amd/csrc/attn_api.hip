@@ -109,7 +109,9 @@ int norm_rope_args(const Heads* q, const Heads* k, gptq_dtype dt, int64_t tokens
   bool vec = true;
   if ((st = side_check(q, dt, tokens > 0, &a->q, &vec)) != GPTQ_OK) return st;
   if ((st = side_check(k, dt, tokens > 0, &a->k, &vec)) != GPTQ_OK) return st;
-  if (tokens > 0 && a->q.heads + a->k.heads > 0 && rope->rot > 0 && (!positions || !aligned(positions, 4)))
+  // a position out of range is replaced by 0, so there has to be a row 0 of cos and sin
+  if (tokens > 0 && a->q.heads + a->k.heads > 0 && rope->rot > 0 &&
+      (!positions || !aligned(positions, 4) || rope->max_pos < 1))
     return GPTQ_EINVAL;
   if (!aligned(d_status, 4)) return GPTQ_EINVAL;
   // an item (token and heads) and a thread of it are counted in 32 bits

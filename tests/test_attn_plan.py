@@ -52,3 +52,19 @@ BIG = 1 << 30
 ])
 def test_calls_past_what_a_launch_holds_are_refused(n, max_new, q_heads, kv_heads, max_kv):
     assert attend(cache(kv_heads), batch(n, BIG, max_new, max_kv), q_heads) == g.GPTQ_EUNSUPPORTED
+
+
+def norm_rope(tokens, max_pos, backward=False, rot=64):
+    r = attn.gptq_rope(A, A, max_pos, rot, 0, 1e-6)
+    if backward:
+        side = attn.gptq_heads_grad(A, 512, 128, 2 * A, 512, 128, 3 * A, 512, 128, None, None, 4)
+        return g.lib().gptq_qk_norm_rope_backward(side, None, 0, tokens, 128, A, r, None, 0, None, None)
+    return g.lib().gptq_qk_norm_rope(attn.gptq_heads(A, 512, 128, 2 * A, 512, 128, None, 4), None, 0, tokens, 128, A, r,
+                                     None, None)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_tables_without_positions_are_refused(backward):
+    """No position is in range of cos and sin without rows, nor is there a row to read in its place."""
+    assert norm_rope(3, 0, backward) == g.GPTQ_EINVAL
+    assert norm_rope(0, 0, backward) == g.GPTQ_OK
