@@ -2,7 +2,7 @@
 // and its gradients.
 //
 //   r = (mean x^2 + eps)^-1/2,  n = x r w,  y = R(p) n
-//   dn = R(p)^T dy,  g = dn w,  dx = r g - x r^3 mean(g x),  dw = sum dn x r
+//   dn = R(p)^T dy,  g = dn w,  dx = r (g - x r mean(g x r)),  dw = sum dn x r
 //
 // Every element is read once and written once (backward: two read, one
 // written) and some ten operations are done on it, so HBM bounds both.  A lane
@@ -148,17 +148,18 @@ __global__ __launch_bounds__(NR_THREADS) void k_norm_rope_bwd(NormRope A, int L,
       float gx = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        da[j] = fmaf(ga[j], xa[j] * r, da[j]);
-        db[j] = fmaf(gb[j], xb[j] * r, db[j]);
+        xa[j] *= r, xb[j] *= r;  // of size 1 from here on: r^3 leaves fp32's range long before dx does
+        da[j] = fmaf(ga[j], xa[j], da[j]);
+        db[j] = fmaf(gb[j], xb[j], db[j]);
         ga[j] *= wa[j];
         gb[j] *= wb[j];
         gx = fmaf(ga[j], xa[j], fmaf(gb[j], xb[j], gx));
       }
-      const float c = r * r * r * (head_sum(gx, L) * inv_dim);
+      const float c = head_sum(gx, L) * inv_dim;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        ga[j] = fmaf(-xa[j], c, r * ga[j]);
-        gb[j] = fmaf(-xb[j], c, r * gb[j]);
+        ga[j] = r * fmaf(-xa[j], c, ga[j]);
+        gb[j] = r * fmaf(-xb[j], c, gb[j]);
       }
     }
     if (live) {

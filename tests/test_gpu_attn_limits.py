@@ -3,8 +3,9 @@
 import numpy as np
 import pytest
 
-from attnhelp import Paged, on_device, values
+from attnhelp import H, U, Paged, close, on_device, values
 from gpuhelp import say, torch_dev
+from oracle import attn_ref as R
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +26,26 @@ def test_windows_longer_than_any_sequence(new, causal):
     for window in (5000, (1 << 63) - 1 - new, (1 << 63) - 1):
         got, lse = g.gptq_kv_attention(q, c.dev, plan, causal=causal, window=window, want_lse=True)
         assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("size", [0.0, 1e-14, 1e-3, 1e14])
+def test_gradients_of_inputs_far_from_one(size, bf16):
+    """dx of inputs so small or large that r^3 or its product with x alone passes fp32's range, though dx does not.
+    Bounds as in test_gpu_qk_norm_rope.py, without rotation."""
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    say(f"gradients of inputs of size {size}, bf16={bf16}")
+    rng = np.random.default_rng(62)
+    eps = 1e-30
+    x = values(rng, (9, 3, 128), bf16, size or 1.0) * (1.0 if size else 0.0)
+    dy, w = values(rng, x.shape, bf16), values(rng, (128,), bf16, 0.3)
+    want, want_w = R.norm_rope_backward(dy, x, w, np.zeros((1, 0)), np.zeros((1, 0)), np.zeros(9, int), False, eps)
+    dx, _, dw, _ = g.gptq_qk_norm_rope_backward(on_device(dy, bf16), None, on_device(x, bf16), None, None,
+                                                g.Rope(None, None, False, eps), on_device(w[None, None], bf16)[0, 0])
+    r = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    gm = np.abs(w * dy)
+    bound = (H if bf16 else U) * np.abs(want) + 44 * U * r * gm + \
+        152 * U * np.abs(x) * r ** 3 * (gm * np.abs(x)).mean(-1, keepdims=True) + 1e-40
+    close("dx", dx.float().cpu().numpy(), want, bound)
+    close("dw", dw.cpu().numpy(), want_w, 2 * (20 + 60) * U * (np.abs(dy * x) * r).sum((0, 1)) + 1e-40)
