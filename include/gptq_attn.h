@@ -71,7 +71,7 @@ int gptq_qk_norm_rope(const gptq_heads* q, const gptq_heads* k, gptq_dtype dtype
 
 /* Gradients: dx of type dtype from dy and the forward's x, and, where weight is
  * given, dweight (fp32 [dim], written) summed over tokens and heads in a fixed
- * order (bit-reproducible).  weight NULL: dx is dy rotated back and x, dweight
+ * order (bit-reproducible); heads 0: dweight := 0, the other pointers may be NULL.  weight NULL: dx is dy rotated back and x, dweight
  * are not used (may be NULL).  dx may be dy with the same strides. */
 typedef struct {
   const void* dy;
@@ -85,7 +85,7 @@ typedef struct {
   int32_t heads;
 } gptq_heads_grad;
 
-/* Device bytes for gptq_qk_norm_rope_backward (0 without weights). */
+/* Device bytes for gptq_qk_norm_rope_backward with weights (without any, it takes none). */
 size_t gptq_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int32_t dim, int32_t q_heads, int32_t k_heads);
 
 /* tokens == 0: dweight := 0, nothing else.  workspace 4-byte aligned. */

@@ -78,7 +78,11 @@ int side_check(const gptq_heads* s, gptq_dtype dt, bool any, HeadSide* out, bool
 }
 int side_check(const gptq_heads_grad* s, gptq_dtype dt, bool any, HeadSide* out, bool* vec) {
   *out = HeadSide{};
-  if (!s || s->heads == 0) return GPTQ_OK;
+  if (!s) return GPTQ_OK;
+  if (s->heads == 0) {
+    out->weight = s->weight;  // its gradient is written: 0
+    return aligned(s->dweight, 4) ? GPTQ_OK : GPTQ_EINVAL;
+  }
   if (s->heads < 0 || s->heads > 65536 || (any && (!s->dy || !s->dx || (s->weight && !s->x)))) return GPTQ_EINVAL;
   if (!stride_ok(s->dy_token) || !stride_ok(s->dy_head) || !stride_ok(s->dx_token) || !stride_ok(s->dx_head) ||
       (s->weight && (!stride_ok(s->x_token) || !stride_ok(s->x_head))))
@@ -156,7 +160,7 @@ int gptq_qk_norm_rope_backward(const gptq_heads_grad* q, const gptq_heads_grad* 
   float* dqw = a.q.weight ? q->dweight : nullptr;
   float* dkw = a.k.weight ? k->dweight : nullptr;
   if ((tokens == 0 || a.q.heads + a.k.heads == 0) && !dqw && !dkw) return GPTQ_OK;
-  if (a.q.weight || a.k.weight) {
+  if ((a.q.weight && a.q.heads) || (a.k.weight && a.k.heads)) {
     const size_t need = gptq_qk_norm_rope_backward_workspace_bytes(tokens, dim, a.q.heads, a.k.heads);
     if (workspace_bytes < need || (need > 0 && !workspace)) return GPTQ_EWORKSPACE;
     if (!aligned(workspace, 4)) return GPTQ_EINVAL;

@@ -68,3 +68,14 @@ def test_tables_without_positions_are_refused(backward):
     """No position is in range of cos and sin without rows, nor is there a row to read in its place."""
     assert norm_rope(3, 0, backward) == g.GPTQ_EINVAL
     assert norm_rope(0, 0, backward) == g.GPTQ_OK
+
+
+def test_a_side_without_heads_needs_no_workspace():
+    """Its weight's gradient is zero; the other side's gradients without a weight need no sums.  (No tokens, so
+    that the call ends on the host unless the zero is asked for.)"""
+    none = attn.gptq_heads_grad(None, 0, 0, None, 0, 0, None, 0, 0, A, None, 0)
+    other = attn.gptq_heads_grad(A, 512, 128, None, 0, 0, 2 * A, 512, 128, None, None, 4)
+    r = attn.gptq_rope(None, None, 0, 0, 0, 1e-6)
+    assert g.lib().gptq_qk_norm_rope_backward(none, other, 0, 0, 128, None, r, None, 0, None, None) == g.GPTQ_OK
+    none.dweight = A + 2
+    assert g.lib().gptq_qk_norm_rope_backward(none, other, 0, 0, 128, None, r, None, 0, None, None) == g.GPTQ_EINVAL

@@ -49,3 +49,20 @@ def test_gradients_of_inputs_far_from_one(size, bf16):
         152 * U * np.abs(x) * r ** 3 * (gm * np.abs(x)).mean(-1, keepdims=True) + 1e-40
     close("dx", dx.float().cpu().numpy(), want, bound)
     close("dw", dw.cpu().numpy(), want_w, 2 * (20 + 60) * U * (np.abs(dy * x) * r).sum((0, 1)) + 1e-40)
+
+
+@pytest.mark.parametrize("side", ["q", "k"])
+def test_a_side_without_heads_has_a_weight_gradient_of_zero(side):
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    rng = np.random.default_rng(63)
+    x = on_device(values(rng, (5, 3, 64), False), False)
+    none = x[:, :0]
+    w = torch.ones(64, device=dev)
+    for _ in range(3):  # what the allocator hands out next is not zero
+        [torch.full((64,), 7.0, device=dev) for _ in range(16)]
+        sides = (none, x, none, x) if side == "q" else (x, none, x, none)
+        dq, dk, dqw, dkw = g.gptq_qk_norm_rope_backward(*sides, None, g.Rope(None, None), w, w)
+        empty, full = (dqw, dkw) if side == "q" else (dkw, dqw)
+        assert torch.equal(empty, torch.zeros_like(empty))
+        assert not torch.equal(full, torch.zeros_like(full))
