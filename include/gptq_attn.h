@@ -103,7 +103,8 @@ int gptq_qk_norm_rope_backward(const gptq_heads_grad* q, const gptq_heads_grad* 
  *   k_scales, v_scales fp32 [pages][kv_heads]
  * block 16, 32, 64 or 128; dim 64, 128 or 256 (else GPTQ_EUNSUPPORTED).
  * Code pointers 16-byte aligned.  Nothing has to be cleared before first use.
- * Scales are not negative; gptq_kv_append writes powers of two, or NaN. */
+ * Scales are not negative and at most 2^122; gptq_kv_append writes powers of two
+ * from 2^-100 on, or NaN. */
 typedef struct {
   int8_t* k_codes;
   int8_t* v_codes;
@@ -170,10 +171,13 @@ int gptq_kv_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch, void* k
  *   lse     fp32 [total, q_heads], contiguous; NULL: not written
  * Products run on the matrix cores with fp32 accumulation.  Codes are exact in
  * fp16.  A bf16 query, scaled by a power of two of its row, is exact in fp16 as
- * far as 2^-22 of the row's largest element; weights are rounded to fp16 (2^-11)
- * before the second product.  For fp32, query and weights go in two fp16 parts
- * each (about 2^-22).  Maximum, sum and output are kept in fp32.  Results are
- * bit-reproducible run to run.
+ * far as 2^-22 of the row's largest element; weights times their block's value
+ * scale are rounded to fp16 (2^-11) before the second product.  For fp32, query
+ * and weights go in two fp16 parts each (about 2^-22).  fp16's range is set, row by
+ * row, by the largest product of weight and value scale that the row sees: products
+ * are held to 2^-31 of that, whatever is in blocks that the row does not see.
+ * Maximum, sum and output are kept in fp32; lse does not depend on values.  Results
+ * are bit-reproducible run to run.
  * workspace: gptq_kv_attention_workspace_bytes(...) bytes, 16-byte aligned: the
  * partial results of calls that split long sequences.  out must not overlap q,
  * the cache or the workspace.  q_heads: a multiple of kv_heads. */

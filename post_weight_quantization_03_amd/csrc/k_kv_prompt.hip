@@ -28,9 +28,10 @@
 //
 // The softmax is an fma, an exponential and an addition a score: the key scale
 // times the row's constant is one factor, the maximum is taken before it (it is not
-// negative), the value scale is added to the exponent (log2 of its ratio to the
-// largest so far) and taken back out of the sum once for 16 tokens, and output and
-// sum are rescaled only when a row's maximum has grown by more than 2^8.  Sums are of
+// negative), the value scale is added to the exponent (kv_attend.h) and taken back
+// out of the sum once for 16 tokens, and output and sum are rescaled only when a
+// row's maximum has grown by more than 2^7.  Tiles with a value scale that is no power of two, not finite or 2^80
+// below the largest take one more multiplication a score, as do those with masked places.  Sums are of
 // the unrounded weights (of the rounded ones, two at a time, lse lost 1e-4).
 #include "kv_attend.h"
 
@@ -42,12 +43,8 @@ namespace {
 
 constexpr int PT = 64;                // tokens a tile
 constexpr int SB = 8;                 // tiles whose scales are brought in together
-constexpr float P_EXP = 6.0f;         // weights are 2^P_EXP e^(s - m), m up to 2^P_SLACK behind the maximum
-constexpr float P_SLACK = 8.0f;
-constexpr float P_LOG_MIN = -200.0f;  // log2 of a value scale, at least
-constexpr float P_RATIO_MIN = -60.0f; // log2 of its ratio to the largest, at least: below, fp16 weights are 0
-
-__device__ __forceinline__ float keep_nan_max(float x, float lo) { return x != x ? x : fmaxf(x, lo); }
+constexpr float P_EXP = 7.0f;         // weights are up to 2^P_EXP in fp16, or
+constexpr float P_SLACK = 7.0f;       // 2^(P_EXP + P_SLACK) while m is up to P_SLACK behind the row's maximum
 
 // Maximum and sum over the two lanes of a column: v_permlane32_swap of x with itself leaves the lower
 // half's values in one register and the upper half's in the other (VALU; a shuffle would wait behind the
@@ -73,12 +70,15 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   constexpr int KC = KROW / 16;        // 16-byte pieces a K row
   constexpr int KB = PT * KROW, VB = DIM * VROW;
   __shared__ __align__(16) char lds[2 * (KB + VB)];  // [2][KB], [2][VB]
-  // of a tile's four groups of 16 tokens: key scale, log2 of the value scale's ratio to the
-  // largest so far and the inverse of that ratio; log2 of the largest so far
+  // Of a tile's four groups of 16 tokens: key scale, the value scale's exponent lv and 2^(KV_C - P_EXP - lv); a bit
+  // for each group of value scale 2^lv, near the largest.  Beside it the value scales, for tiles in which not all
+  // are so.
   struct Scales {
-    float ks[4], lr[4], ir[4], lref, pad[3];
+    float ks[4], lv[4], zl[4];
+    int plain, pad[3];
   };
   __shared__ __align__(16) Scales sc[2 * SB];
+  __shared__ __align__(16) f32x4 value_scales[2 * SB];
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 31, half = lane >> 5;
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   for (int d = 0; d < ND; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-  float m = -INFINITY, l = 0.0f, lref = P_LOG_MIN;
+  float m = -INFINITY, l = 0.0f;
 
   // A thread's pieces of the tiles to come.  The 64 pieces of a wave lie in one group of 16 tokens, for K
   // and for V, so their page is one number a wave, read a tile ahead of the pieces, which thus never wait for
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   // looked up, scales read and the result placed in different turns, a batch ahead of its use.  The largest
   // value scale so far is taken over the whole batch.
   int page_s = 0;
-  float next_ks = 0.0f, next_vs = 0.0f, run_ref = P_LOG_MIN;
+  float next_ks = 0.0f, next_vs = 0.0f, lv_most = KV_LV_MIN;
   auto look_s = [&](int batch) INLINE { page_s = entry(t0 + PT * SB * batch + 16 * (lane & (4 * SB - 1))); };
   auto fetch_s = [&](int batch) INLINE {
     const bool ok = (uint32_t)page_s < (uint32_t)A.cache.pages;
@@ -237,25 +237,30 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     if (t0 + PT * SB * batch + 16 * (lane & (4 * SB - 1)) >= t1) next_vs = 0.0f;
   };
   auto place_s = [&](int batch) INLINE {
-    const float lv = keep_nan_max(__log2f(next_vs), P_LOG_MIN);
-    run_ref = fmaxf(run_ref, lv);
+    const float lv = value_exponent(next_vs);
+    lv_most = fmaxf(lv_most, lv);
 #pragma unroll
-    for (int k = 1; k < 4 * SB; k *= 2) run_ref = fmaxf(run_ref, __shfl_xor(run_ref, k));
-    const float lr = keep_nan_max(lv - run_ref, P_RATIO_MIN);
-    Scales& S = sc[SB * (batch & 1) + (lane >> 2 & (SB - 1))];
+    for (int k = 1; k < 4 * SB; k *= 2) lv_most = fmaxf(lv_most, __shfl_xor(lv_most, k));
+    const int g = lane & 3, at = SB * (batch & 1) + (lane >> 2 & (SB - 1));
+    int plain = lv >= lv_most - KV_NEAR && next_vs == ldexpf(1.0f, (int)lv) ? 1 << g : 0;
+    plain |= __shfl_xor(plain, 1);
+    plain |= __shfl_xor(plain, 2);
     if (lane < 4 * SB) {
-      S.ks[lane & 3] = next_ks;
-      S.lr[lane & 3] = lr;
-      // with a scale of NaN the weights that see it are NaN; the sums of rows that do not are 0
-      S.ir[lane & 3] = lr != lr ? 1.0f : exp2_fast(-lr);
-      S.lref = run_ref;
+      sc[at].ks[g] = next_ks;
+      sc[at].lv[g] = lv;
+      sc[at].zl[g] = ldexpf(1.0f, (int)(KV_C - P_EXP - lv));
+      sc[at].plain = plain;
+      value_scales[at][g] = next_vs;
     }
   };
 
   f16x8 ph[4], pl[BF16 ? 1 : 4];  // a tile's weights, from its softmax to its output
   Scales S;                       // its scales, read with the last operands of its scores
-  auto softmax = [&]<bool MASKED>(int tile, f32x16 (&x)[2]) INLINE {
-    if constexpr (MASKED) {
+  // ANY: with masked places or scales of any kind
+  auto softmax = [&]<bool ANY>(int tile, f32x16 (&x)[2]) INLINE {
+    f32x4 vs;
+    if constexpr (ANY) {
+      vs = value_scales[tile & (2 * SB - 1)];
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
@@ -264,7 +269,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
           x[tt][i] = j >= see.lo && j < see.hi ? x[tt][i] : -INFINITY;
         }
     }
-    float f[4], most = -INFINITY;
+    float f[4], top[4], most = -INFINITY;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       f[g] = S.ks[g] * qs;
@@ -273,41 +278,45 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
       const float y = fmaxf(fmaxf(fmaxf(fmaxf(z[e], z[e + 1]), z[e + 2]), fmaxf(fmaxf(z[e + 3], z[e + 4]), z[e + 5])),
                             fmaxf(z[e + 6], z[e + 7]));
       // a masked group stays out whatever its factor is (0, infinite or NaN)
-      most = fmaxf(most, MASKED && y == -INFINITY ? y : y * f[g]);
+      if constexpr (ANY) top[g] = y == -INFINITY ? y : y * f[g];
+      most = fmaxf(most, ANY ? top[g] + S.lv[g] : fmaf(y, f[g], S.lv[g]));
     }
     most = column_max(most);
-    const float mn = fmaxf(m, most);
-    if (__any(mn > m + P_SLACK || (m == -INFINITY && mn != m)) || S.lref != lref) {
-      const float base = mn == -INFINITY ? 0.0f : mn;
-      const float alpha = exp2_fast(m - base);
-      l *= alpha;
-      const float turn = alpha * exp2_fast(lref - S.lref);
+    if (__any(most > m + P_SLACK)) {
+      const float mn = fmaxf(m, ceilf(most));
+      const Decay turn = decay(m - (mn == -INFINITY ? 0.0f : mn));
+      l = l * turn.half * turn.half;
 #pragma unroll
-      for (int d = 0; d < ND; ++d) o[d] *= turn;
+      for (int d = 0; d < ND; ++d) o[d] *= turn.all;
       m = mn;
-      lref = S.lref;
     }
     const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const float add = (P_EXP - base) + S.lr[g];
+      const float k = !ANY ? P_EXP + S.lv[g] : top[g] == -INFINITY ? 0.0f : ceilf(base - top[g]);
+      const float add = k - base;
       float p[8], sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float y = x[g >> 1][8 * (g & 1) + i];
         float e = exp2_fast(fmaf(y, f[g], add));
-        if constexpr (MASKED) e = y == -INFINITY ? 0.0f : e;
+        if constexpr (ANY) e = y == -INFINITY ? 0.0f : e;
         p[i] = e;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += p[i];
+      if constexpr (ANY) {
+        const float zp = ldexpf(vs[g], (int)(P_EXP - k));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = x[g >> 1][8 * (g & 1) + i] == -INFINITY ? 0.0f : p[i] * zp;
+      }
       if constexpr (BF16) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) ph[g][i] = (_Float16)p[i];
       } else {
         split16(p, ph[g], pl[g]);
       }
-      l = fmaf(sum, S.ir[g], l);
+      l = ANY ? l + ldexpf(sum, (int)(KV_C - k)) : fmaf(sum, S.zl[g], l);
     }
   };
   // The matrix products of a turn: output of the tile before (PV), scores of this one (QK).  Their LDS operands
@@ -405,7 +414,9 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     f32x16 x[2];
     auto weigh = [&](int tile) INLINE {
       const int t = t0 + PT * tile;
-      if (t >= full_lo && t + PT <= full_hi)
+      // one condition of vector registers, though it is the same in all lanes: as a scalar branch the compiler reads
+      // ahead across it, and spills (188 bytes a lane at dim 128)
+      if ((t >= full_lo) & (t + PT <= full_hi) & (S.plain == 15))
         softmax.template operator()<false>(tile, x);
       else
         softmax.template operator()<true>(tile, x);
@@ -443,8 +454,8 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
 
   l = column_sum(l);
   if (r >= rows) return;
-  const float inv = l == 0.0f ? 0.0f : exp2_fast(lref) / l;
-  const float lse2 = l == 0.0f ? -INFINITY : m + __log2f(l) - P_EXP;
+  const float inv = l == 0.0f ? 0.0f : exp2_fast(KV_C - P_EXP) / l;
+  const float lse2 = log2_sum(m, l);
   const int64_t token = s.row + r / group;
   const int head = hk * group + r % group;
   const int64_t at = (token * A.a.q_heads + head) * P.nsplit + split;

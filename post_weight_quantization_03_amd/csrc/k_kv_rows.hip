@@ -24,15 +24,15 @@
 // joining 64 splits; over 43 tokens 7.4 us, the latencies of lengths, table, cache and output in turn.
 // Three waves a SIMD instead of two spill: 707 us for the first.
 //
-// Scales: K's multiplies the score.  V's enters the weight as its ratio to the
-// largest seen so far (like the running maximum), so fp16 weights keep their range
-// whatever the scales are.
+// Scales: K's multiplies the score (the factor is not negative, so a row's maximum is taken before it), V's goes
+// into the exponent of the weight (kv_attend.h).
 #include "kv_attend.h"
 
 namespace gptq {
 namespace {
 
 constexpr int KW = 4;  // waves
+constexpr float P_EXP = 14.0f;  // weights are up to 2^P_EXP in fp16, normal numbers down to 2^-28 of that
 
 template <int DIM, bool BF16, int CT>
 __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAttention A, Partials P, uint32_t row_tiles) {
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   constexpr int CW = DIM < 128 ? DIM : 128;  // columns joined at a time
   constexpr int LDO = CW + 4;
   __shared__ __align__(16) float so[KW][16 * LDO];
-  __shared__ float sm[KW][16 * CT], sl[KW][16 * CT], sr[KW][16 * CT];
+  __shared__ float sm[KW][16 * CT], sl[KW][16 * CT];
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n16 = lane & 15, g = lane >> 4;
@@ -141,7 +141,8 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
     most = fmaxf(most, __shfl_xor(most, 32));
     float up, down;
     row_scale(most, up, down);
-    qs[c] = A.a.sm_scale * 1.44269504088896340736f * down;
+    qs[c] = fabsf(A.a.sm_scale) * 1.44269504088896340736f * down;
+    if (A.a.sm_scale < 0.0f) up = -up;  // the factor of a score is not negative
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
 #pragma unroll
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   }
 
   f32x4 o[CT][ND];
-  float m[CT], l[CT], ref = 0.0f;
+  float m[CT], l[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     m[c] = -INFINITY;
@@ -196,38 +197,37 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
     const float vs_now = t + 16 * g < t_stop ? vs : 0.0f;
     if (tn < t_stop) load_k(tn);
 
-    // V's scales against the largest seen so far
-    float rt_max = fmaxf(vs_now, __shfl_xor(vs_now, 16));
-    rt_max = fmaxf(rt_max, __shfl_xor(rt_max, 32));
-    const float ref_new = fmaxf(ref, rt_max);
-    const float ref_inv = ref_new > 0.0f ? 1.0f / ref_new : 0.0f;
-    const float vratio = vs_now * ref_inv, oratio = ref * ref_inv;
-    ref = ref_new;
-
+    const float lv = value_exponent(vs_now);
     const bool full = t >= full_lo && t + 64 <= full_hi;
     f16x8 ph[CT][2], pl[CT][BF16 ? 1 : 2];
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
       const float f = ks_now * qs[c];
-      float most = -INFINITY;
+      if (!full) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = t + 16 * g + 4 * tt + r;
+            x[c][tt][r] = j >= see[c].lo && j < see[c].hi ? x[c][tt][r] : -INFINITY;
+          }
+      }
+      float top = -INFINITY;  // of the 16 scores
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float y = x[c][tt][r] * f;
-          if (!full) {
-            const int j = t + 16 * g + 4 * tt + r;
-            y = j >= see[c].lo && j < see[c].hi ? y : -INFINITY;
-          }
-          x[c][tt][r] = y;
-          most = fmaxf(most, y);
-        }
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, x[c][tt][r]);
+      // a masked group stays out whatever its factor is (0, infinite or NaN)
+      top = top == -INFINITY ? top : top * f;
+      float most = top + lv;
       most = fmaxf(most, __shfl_xor(most, 16));
       most = fmaxf(most, __shfl_xor(most, 32));
-      const float mn = fmaxf(m[c], most);
+      const float mn = fmaxf(m[c], ceilf(most));
       const float base = mn == -INFINITY ? 0.0f : mn;
-      const float alpha = exp2_fast(m[c] - base);
+      const Decay turn = decay(m[c] - base);
       m[c] = mn;
+      const float k = top == -INFINITY ? 0.0f : ceilf(base - top);
+      const float add = k - base, zp = ldexpf(vs_now, (int)(P_EXP - k));
       float sum = 0.0f;
       float p[16];
 #pragma unroll
@@ -235,16 +235,14 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float y = x[c][tt][r];
-          const float e = exp2_fast(y - base + KV_PEXP);
+          float e = exp2_fast(fmaf(y, f, add));
+          if (!full) e = y == -INFINITY ? 0.0f : e;  // also where the block's scale of keys is NaN
           sum += e;
-          float w = e * vratio;
-          if (!full) w = y == -INFINITY ? 0.0f : w;  // also where the block's scale is NaN
-          p[4 * tt + r] = w;
+          p[4 * tt + r] = full || y != -INFINITY ? e * zp : 0.0f;  // and where that of values is
         }
-      l[c] = l[c] * alpha + sum;
-      const float turn = alpha * oratio;
+      l[c] = l[c] * turn.half * turn.half + ldexpf(sum, (int)(KV_C - k));
 #pragma unroll
-      for (int d = 0; d < ND; ++d) o[c][d] *= turn;
+      for (int d = 0; d < ND; ++d) o[c][d] *= turn.all;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float q8[8];
@@ -282,7 +280,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   for (int c = 0; c < CT; ++c) {
     l[c] += __shfl_xor(l[c], 16);
     l[c] += __shfl_xor(l[c], 32);
-    if (g == 0) sm[wave][16 * c + n16] = m[c], sl[wave][16 * c + n16] = l[c], sr[wave][16 * c + n16] = ref;
+    if (g == 0) sm[wave][16 * c + n16] = m[c], sl[wave][16 * c + n16] = l[c];
   }
 #pragma unroll
   for (int c = 0; c < CT; ++c)
@@ -306,16 +304,15 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
         for (int j = 0; j < 8; ++j) y[j] = 0.0f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const float f = exp2_fast(sm[w][16 * c + row] - base);
-          const float fo = f * sr[w][16 * c + row];
-          sum = fmaf(f, sl[w][16 * c + row], sum);
+          const Decay turn = decay(sm[w][16 * c + row] - base);
+          sum += sl[w][16 * c + row] * turn.half * turn.half;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = fmaf(fo, so[w][row * LDO + d + j], y[j]);
+          for (int j = 0; j < 8; ++j) y[j] = fmaf(turn.all, so[w][row * LDO + d + j], y[j]);
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a sum of NaN stays NaN
+        const float inv = sum == 0.0f ? 0.0f : exp2_fast(KV_C - P_EXP) / sum;  // a sum of NaN stays NaN
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] *= inv;
-        const float lse2 = sum == 0.0f ? -INFINITY : mm + __log2f(sum) - KV_PEXP;
+        const float lse2 = log2_sum(mm, sum);
         const int64_t token = s.row + r / group;
         const int head = hk * group + r % group;
         if (whole) {

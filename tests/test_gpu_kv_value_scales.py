@@ -1,0 +1,212 @@
+"""GPU tests of gptq_kv_attention over caches whose blocks' value scales differ: a row's result is as near to the
+fp64 reference as what the row itself sees allows, whatever the scales of blocks that it does not see, or sees
+with no weight to speak of.
+
+Bound of out.  A score is off by ds = (dim + 8) 2u smag, and a weight by 2^-20 more for its exponential.  Weights
+times their block's value scale are rounded to fp16 (F; two parts: 2^-21), and where they are below fp16's normal
+numbers by 2^-31 of the row's largest such product (2^6 at least in fp16, whose least step is 2^-24).  Sums
+over the n tokens that a row sees are accumulated in fp32 (n 2u), and the result is rounded once.  All of it is
+relative to what the row sees: its weights times |v|, and for the fp16 floor 128 times its largest product of
+weight and scale.  lse: ds, the exponential, the sum, and 8 u of its size.
+"""
+
+import numpy as np
+import pytest
+
+from attnhelp import F, H, U, Paged, close, on_device, values
+from gpuhelp import say, to_dev, torch_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(c, b, q, length, sm_scale, causal, window, bf16):
+    """(out, lse, bound of out, bound of lse, sees) of one sequence; sees [n, length]."""
+    n, qh, dim = q.shape
+    k, v = c.kv(b, length)
+    step = np.repeat(c.ref.v_scales[c.table[b, :-(-length // c.block)]], c.block, 0)[:length]
+    j, p = np.arange(length), np.arange(length - n, length)[:, None]
+    sees = (j <= p) if causal else np.ones((n, length), bool)
+    if window:
+        sees = sees & (j > p - window)
+    out, lse = np.zeros(q.shape), np.full((n, qh), -np.inf)
+    ob, lb = np.zeros(q.shape), np.ones((n, qh))
+    any_ = sees.any(1)
+    count = sees.sum(1)[any_, None]
+    for h in range(qh):
+        kk, vv, ss = (t[:, h // (qh // c.kv_heads)] for t in (k, v, step))
+        s = np.where(sees, q[:, h] @ kk.T * sm_scale, -np.inf)[any_]
+        smag = np.where(sees, np.abs(q[:, h]) @ np.abs(kk).T, 0)[any_].max(1, keepdims=True) * abs(sm_scale)
+        most = s.max(1, keepdims=True)
+        w = np.exp(s - most)
+        total = w.sum(1, keepdims=True)
+        w /= total
+        o = w @ vv
+        top = (w * ss).max(1, keepdims=True)
+        ds = (dim + 8) * 2 * U * smag + 2.0 ** -20
+        rel = 1.1 * (2 * ds + (F if bf16 else 2.0 ** -21) + count * 2 * U)
+        out[any_, h], lse[any_, h] = o, (most + np.log(total))[:, 0]
+        ob[any_, h] = rel * (w @ np.abs(vv)) + count * 2.0 ** -31 * 128 * top + (H if bf16 else 4 * U) * np.abs(o)
+        lb[any_, h] = (1.1 * ds + count * 2 * U + 8 * U * (1 + np.abs(most + np.log(total))))[:, 0]
+    return out, lse, ob + 1e-38, lb, sees
+
+
+def scales(c, k=None, v=None):
+    """Gives the blocks these scales [pages, heads], on the device and in the oracle."""
+    for name, x in (("k_scales", k), ("v_scales", v)):
+        if x is not None:
+            setattr(c.ref, name, np.asarray(x, dtype=np.float32).astype(np.float64))
+            getattr(c.dev, name).copy_(to_dev(np.asarray(x, dtype=np.float32)))
+
+
+def check(c, new, qh, bf16, causal=True, window=0, lengths=None, qscale=1.0, sm_scale=None, seed=71):
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    rng = np.random.default_rng(seed)
+    lengths = c.lengths if lengths is None else lengths
+    plan, start = c.plan(new, lengths)
+    q = values(rng, (int(start[-1]), qh, c.dim), bf16, qscale)
+    out, lse = g.gptq_kv_attention(on_device(q, bf16), c.dev, plan, sm_scale, causal, window, want_lse=True)
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    sm = c.dim ** -0.5 if sm_scale is None else sm_scale
+    for b, n in enumerate(new):
+        rows = slice(start[b], start[b + 1])
+        want, want_lse, ob, lb, sees = reference(c, b, q[rows], lengths[b], sm, causal, window, bf16)
+        close(f"out[{b}]", out[rows], want, ob)
+        seen = sees.any(1)
+        assert np.all(out[rows][~seen] == 0) and np.all(np.isneginf(lse[rows][~seen]))
+        close(f"lse[{b}]", lse[rows][seen], want_lse[seen], lb[seen])
+
+
+SHAPES = [  # new tokens, dim, block: row tiles of 16, 32, 128 and 256 rows, of each head size
+    (5, 64, 16), (30, 64, 32), (150, 64, 16), (9, 128, 16), (30, 128, 64), (60, 128, 16), (300, 128, 32),
+    (5, 256, 16), (150, 256, 64)]
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("k", [16, 28, 40, 90])
+def test_a_later_block_of_large_values(shape, bf16, k):
+    """The last block's values are 2^k times as large: rows before it do not see it."""
+    new, dim, block = shape
+    say(f"a later block 2^{k} as large, {shape} bf16={bf16}")
+    rng = np.random.default_rng(72)
+    c = Paged(rng, [new + 33], 2, block, dim)
+    v = c.ref.v_scales.copy()
+    v[c.table[0, (new + 32) // block]] *= 2.0 ** k
+    v[~np.isfinite(v)] = 1.0
+    scales(c, v=v)
+    check(c, [new], 4, bf16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("mask", [(True, 0), (True, 40), (False, 70)])
+def test_blocks_of_any_size(shape, bf16, mask):
+    """Value scales over 2^80, whatever the order, and scores spread so that the largest values often have next to
+    no weight."""
+    new, dim, block = shape
+    say(f"scales over 2^80, {shape} bf16={bf16} mask={mask}")
+    rng = np.random.default_rng(73)
+    c = Paged(rng, [new + 130, new], 2, block, dim)
+    scales(c, v=2.0 ** rng.integers(-50, 31, c.ref.v_scales.shape))
+    check(c, [new, new], 4, bf16, *mask)
+    check(c, [new, new], 4, bf16, *mask, qscale=6.0)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("form", [([5000, 40, 1300], [1, 1, 1], 4, 2, 128, 64), ([3000], [2], 8, 8, 64, 16),
+                                  ([2100, 10], [40, 10], 4, 1, 128, 32), ([1600], [4], 2, 1, 256, 128),
+                                  ([2500, 90], [70, 70], 4, 2, 64, 128), ([3000, 700], [150, 20], 4, 2, 128, 64)])
+def test_split_sequences_with_blocks_of_any_size(form, bf16):
+    lengths, new, qh, kh, dim, block = form
+    say(f"split, scales over 2^80 {form} bf16={bf16}")
+    rng = np.random.default_rng(74)
+    c = Paged(rng, lengths, kh, block, dim)
+    scales(c, v=2.0 ** rng.integers(-50, 31, c.ref.v_scales.shape))
+    check(c, new, qh, bf16, qscale=3.0)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("ends", [(-100, 122), (122, -100), (122, 122), (-100, -100)])
+def test_scales_at_the_ends_of_their_range(shape, bf16, ends):
+    """The least and the largest scales that an append writes, one after the other: the first half of the blocks has
+    one, the second the other."""
+    new, dim, block = shape
+    say(f"scales 2^{ends[0]} then 2^{ends[1]}, {shape} bf16={bf16}")
+    rng = np.random.default_rng(75)
+    c = Paged(rng, [new + 130], 2, block, dim)
+    c.ref.v_codes[:] = np.clip(c.ref.v_codes, -31, 31)
+    c.dev.v_codes.copy_(to_dev(c.ref.v_codes))
+    v = np.ones(c.ref.v_scales.shape)
+    blocks = -(-(new + 130) // block)
+    v[c.table[0, :blocks // 2]], v[c.table[0, blocks // 2:blocks]] = 2.0 ** ends[0], 2.0 ** ends[1]
+    scales(c, v=v)
+    check(c, [new], 4, bf16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_scales_that_are_zero_or_no_powers_of_two(shape, bf16):
+    """Any scale that is not negative may stand in a cache of the caller's own making."""
+    new, dim, block = shape
+    say(f"other scales, {shape} bf16={bf16}")
+    rng = np.random.default_rng(76)
+    c = Paged(rng, [new + 130], 2, block, dim)
+    scales(c, k=rng.uniform(0.005, 0.02, c.ref.k_scales.shape), v=rng.uniform(0.001, 0.1, c.ref.v_scales.shape))
+    check(c, [new], 4, bf16)
+    v = c.ref.v_scales.copy()
+    v[rng.random(v.shape) < 0.4] = 0.0
+    scales(c, v=v)
+    check(c, [new], 4, bf16)
+    scales(c, v=np.zeros(v.shape))
+    check(c, [new], 4, bf16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_a_value_scale_that_is_not_finite_reaches_no_log_sum_and_no_other_row(shape, bf16, what):
+    """The scores, and so lse, do not depend on values; rows that do not see the block keep their bits."""
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    new, dim, block = shape
+    say(f"value scale {what}, {shape} bf16={bf16}")
+    rng = np.random.default_rng(77)
+    c = Paged(rng, [new + 130], 2, block, dim)
+    c.dev.v_scales.nan_to_num_(nan=1.0, posinf=1.0)
+    plan, _ = c.plan([new])
+    q = values(rng, (new, 4, dim), bf16)
+    good, lse = g.gptq_kv_attention(on_device(q, bf16), c.dev, plan, window=90, want_lse=True)
+    blk = (130 + new // 2) // block
+    c.dev.v_scales[int(c.table[0, blk]), 0] = what
+    got, got_lse = g.gptq_kv_attention(on_device(q, bf16), c.dev, plan, window=90, want_lse=True)
+    p = np.arange(130, 130 + new)
+    sees = (blk * block <= p) & (blk * block + block - 1 > p - 90)
+    for i in range(new):
+        for h in range(4):
+            if sees[i] and h < 2:
+                assert not torch.isfinite(got[i, h]).any()
+            else:
+                assert torch.equal(got[i, h], good[i, h]) and torch.equal(got_lse[i, h], lse[i, h])
+    _, want, _, bound, _ = reference(c, 0, q, new + 130, dim ** -0.5, True, 90, bf16)
+    close("lse", got_lse.cpu().numpy(), want, bound)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("sizes", [(-100, 122), (-100, -9), (-9, 122), (-60, 30)])
+@pytest.mark.parametrize("qscale", [0.3, 4.0])
+def test_neighbouring_blocks_of_far_sizes(shape, bf16, sizes, qscale):
+    """Blocks of two sizes in turn, so that every row weighs both."""
+    new, dim, block = shape
+    say(f"blocks of 2^{sizes[0]} and 2^{sizes[1]} in turn, {shape} bf16={bf16} qscale={qscale}")
+    rng = np.random.default_rng(78)
+    c = Paged(rng, [new + 130], 2, block, dim)
+    c.ref.v_codes[:] = np.clip(c.ref.v_codes, -31, 31)
+    c.dev.v_codes.copy_(to_dev(c.ref.v_codes))
+    v = np.ones(c.ref.v_scales.shape)
+    for i in range(-(-(new + 130) // block)):
+        v[c.table[0, i]] = 2.0 ** sizes[i % 2]
+    scales(c, v=v)
+    check(c, [new], 4, bf16, qscale=qscale)
