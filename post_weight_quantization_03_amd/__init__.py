@@ -142,14 +142,14 @@ def _check_dev(*ts):
 
 def _workspace(nbytes, like, stream=None):
     """A temporary workspace, freed when the caller drops it.  PyTorch's caching allocator ties a
-    block to the stream current at allocation; when the library's work runs on another stream,
-    the block is recorded on that stream too, so it is not handed out again before that work is
-    done."""
+    block to the stream current at allocation: what that stream still has queued may write to it,
+    and it is handed out again in that stream's order.  So it comes from the stream that the
+    library's work runs on."""
     torch = _torch()
-    ws = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    if stream is None:
+        return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=like.device)
 
 
 # --------------------------------------------------------------------------- entry points

@@ -115,21 +115,29 @@ def _weight(name, w, like):
     return w.data_ptr()
 
 
-def _kept(t, stream):
-    """Ties an output of the binding's own to the stream that writes it."""
-    if stream is not None:
-        t.record_stream(stream)
+def _on(stream, make):
+    """An output of the binding's own, made by `make`: from the stream that writes it (as a
+    workspace), and kept until the caller's stream, which reads it, has done so."""
+    if stream is None:
+        return make()
+    torch = _g._torch()
+    callers = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(callers)
     return t
 
 
 def _empty(shape, like, stream, dtype):
-    return _kept(like.new_empty(shape, dtype=dtype), stream)
+    return _on(stream, lambda: like.new_empty(shape, dtype=dtype))
 
 
 def _empty_as(like, stream, dtype=None):
     """A contiguous tensor of like's shape."""
     torch = _g._torch()
-    return _kept(torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format), stream)
+    if stream is None:
+        return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
+    return _on(stream, lambda: torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format))
 
 
 # --------------------------------------------------------------------------- handles

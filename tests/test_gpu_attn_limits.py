@@ -66,3 +66,34 @@ def test_a_side_without_heads_has_a_weight_gradient_of_zero(side):
         empty, full = (dqw, dkw) if side == "q" else (dkw, dqw)
         assert torch.equal(empty, torch.zeros_like(empty))
         assert not torch.equal(full, torch.zeros_like(full))
+
+
+def test_outputs_of_a_call_on_another_stream_are_not_of_the_callers_freed_memory():
+    """A block that the caller has just freed may still be written by the caller's stream: no output of a call on
+    another stream lies in it."""
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    rng = np.random.default_rng(64)
+    c = Paged(rng, [5000], 4, 64, 128)
+    plan, _ = c.plan([1500])
+    x = on_device(values(rng, (1500, 4, 128), True), True)
+    rope, w = g.Rope(None, None), torch.ones(128, dtype=torch.bfloat16, device=dev)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    calls = {"norm": lambda: g.gptq_qk_norm_rope(x, x, None, rope, w, w, stream=side),
+             "gradients": lambda: g.gptq_qk_norm_rope_backward(x, x, x, x, None, rope, w, w, stream=side)[:2],
+             "read": lambda: g.gptq_kv_read(c.dev, plan, stream=side),
+             "attention": lambda: [g.gptq_kv_attention(x, c.dev, plan, stream=side)]}
+    for name, call in calls.items():
+        say(name)
+        mine = [torch.empty_like(x) for _ in range(6)]
+        freed = {t.data_ptr() for t in mine}
+        del mine
+        outs = call()
+        assert not freed & {t.data_ptr() for t in outs}, name
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [t.clone() for t in outs]
+        torch.cuda.synchronize()
+        outs = call()
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(copies, outs)), name
