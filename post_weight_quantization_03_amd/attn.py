@@ -71,34 +71,50 @@ def bind(L):
 
 # --------------------------------------------------------------------------- helpers
 
-def _raw_stream(stream, like):
-    """The HIP stream of `stream`, or the current one of like's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _g._torch()._C._cuda_getCurrentRawStream(like.device.index)
+def _elsewhere(name, t, device):
+    """The error of a tensor that is not on the call's device."""
+    if not t.is_cuda:
+        return ValueError(f"{name} must be a device tensor")
+    return ValueError(f"{name} is on device {t.get_device()}, the call on {device}: a call's tensors are on one device")
 
 
-def _int32(name, t, shape=None):
+def _where(t, stream):
+    """The device of a call on t, and the HIP stream of `stream` or the device's current one (None: the device is
+    not the current one)."""
+    C = _g._torch()._C
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("the tensors must be device tensors")
+    if stream is not None and stream.device_index != d:
+        raise ValueError(f"the stream is on device {stream.device_index}, the call on {d}: they are on one device")
+    if d != C._cuda_getDevice():
+        return d, None
+    return d, C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+
+
+def _int32(name, t, device, shape=None):
     torch = _g._torch()
-    if t.dtype != torch.int32 or not t.is_cuda or t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.get_device() != device:
+        raise _elsewhere(name, t, device)
+    if t.dtype != torch.int32 or t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be an int32 device tensor with unit stride")
     if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}")
 
 
-def _status(t):
-    if t is None:
-        return None
-    _int32("d_status", t)
+def _status(t, device):
+    _int32("d_status", t, device)
     if t.numel() < 1:
         raise ValueError("d_status must hold one int32")
     return t.data_ptr()
 
 
-def _heads(name, t, dtype=None, shape=None):
+def _heads(name, t, device, dtype=None, shape=None):
     """Checks a [tokens, heads, dim] tensor with unit stride in dim, any strides before it, and returns its strides."""
     s = t.stride()
-    if len(s) != 3 or not t.is_cuda or s[2] != 1 and t.shape[2] > 1:
+    if t.get_device() != device:
+        raise _elsewhere(name, t, device)
+    if len(s) != 3 or s[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name} must be a [tokens, heads, dim] device tensor with unit stride in dim")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype}")
@@ -107,21 +123,36 @@ def _heads(name, t, dtype=None, shape=None):
     return s
 
 
-def _weight(name, w, like):
+def _weight(name, w, like, device):
     if w is None:
         return None
-    if w.dtype != like.dtype or w.dim() != 1 or w.numel() != like.shape[2] or not w.is_cuda or not w.is_contiguous():
+    if w.get_device() != device:
+        raise _elsewhere(name, w, device)
+    if w.dtype != like.dtype or w.dim() != 1 or w.numel() != like.shape[2] or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [dim] device tensor of dtype {like.dtype}")
     return w.data_ptr()
 
 
-def _on(stream, make):
+def _given(name, t, device):
+    """(pointer, bytes) of a workspace."""
+    if t.get_device() != device:
+        raise _elsewhere(name, t, device)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _apart(h, device):
+    """The error of a handle whose tensors are not on the call's device."""
+    return ValueError(f"the {type(h).__name__} is on device {h.device}, the call on {device}: a call's tensors are on "
+                      "one device")
+
+
+def _on(like, stream, make):
     """An output of the binding's own, made by `make`: from the stream that writes it (as a
     workspace), and kept until the caller's stream, which reads it, has done so."""
     if stream is None:
         return make()
     torch = _g._torch()
-    callers = torch.cuda.current_stream()
+    callers = torch.cuda.current_stream(like.device)
     with torch.cuda.stream(stream):
         t = make()
     t.record_stream(callers)
@@ -129,7 +160,7 @@ def _on(stream, make):
 
 
 def _empty(shape, like, stream, dtype):
-    return _on(stream, lambda: like.new_empty(shape, dtype=dtype))
+    return _on(like, stream, lambda: like.new_empty(shape, dtype=dtype))
 
 
 def _empty_as(like, stream, dtype=None):
@@ -137,10 +168,19 @@ def _empty_as(like, stream, dtype=None):
     torch = _g._torch()
     if stream is None:
         return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
-    return _on(stream, lambda: torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format))
+    return _on(like, stream, lambda: torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format))
 
 
 # --------------------------------------------------------------------------- handles
+
+def _one_device(*tensors):
+    """The index of the device that holds all of a handle's tensors."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if d < 0 or t.get_device() != d:
+            raise _elsewhere("a tensor", t, d)
+    return d
+
 
 class Rope:
     """cos and sin [max_pos, rot / 2] (fp32, contiguous) of a position rotation, its pairing, and
@@ -148,13 +188,14 @@ class Rope:
 
     def __init__(self, cos, sin, interleaved: bool = False, eps: float = 1e-6):
         torch = _g._torch()
-        self.cos, self.sin = cos, sin
+        self.cos, self.sin, self.device = cos, sin, None
         if cos is None:
             self.c = gptq_rope(None, None, 0, 0, int(interleaved), eps)
             return
         if (cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape):
             raise ValueError("cos and sin must be fp32 [max_pos, rot / 2]")
         _g._check_dev(cos, sin)
+        self.device = _one_device(cos, sin)
         self.c = gptq_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(interleaved), eps)
 
 
@@ -173,6 +214,7 @@ class KVCache:
             raise ValueError("shape or dtype mismatch")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.pages, self.kv_heads, self.block, self.dim = pages, heads, block, dim
+        self.device = _one_device(k_codes, v_codes, k_scales, v_scales)
         self.c = gptq_kv_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                pages, heads, block, dim)
 
@@ -193,9 +235,10 @@ class KVBatch:
 
     def __init__(self, q_start, kv_len, block_table, total: int, max_new: int, max_kv: int):
         batch = kv_len.shape[0]
-        _int32("kv_len", kv_len, (batch,))
-        _int32("q_start", q_start, (batch + 1,))
-        _int32("block_table", block_table)
+        self.device = _one_device(kv_len, q_start, block_table)
+        _int32("kv_len", kv_len, self.device, (batch,))
+        _int32("q_start", q_start, self.device, (batch + 1,))
+        _int32("block_table", block_table, self.device)
         if block_table.dim() != 2 or block_table.shape[0] != batch:
             raise ValueError("block_table must be [batch, blocks]")
         self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
@@ -213,17 +256,17 @@ def _check_plan(cache, batch):
 
 # --------------------------------------------------------------------------- entry points
 
-def _side(name, x, weight, out, stream):
+def _side(name, x, weight, out, device, stream):
     if x is None:
         return None, None
-    sx = _heads(name, x)
+    sx = _heads(name, x, device)
     if out is None:
         out = _empty_as(x, stream)
         sy = out.stride()
     else:
-        sy = _heads(name + "_out", out, x.dtype, x.shape)
+        sy = _heads(name + "_out", out, device, x.dtype, x.shape)
     return out, gptq_heads(x.data_ptr(), sx[0], sx[1], out.data_ptr(), sy[0], sy[1],
-                           _weight(name + "_weight", weight, x), x.shape[1])
+                           _weight(name + "_weight", weight, x, device), x.shape[1])
 
 
 def gptq_qk_norm_rope(q, k, positions, rope: Rope, q_weight=None, k_weight=None, q_out=None, k_out=None,
@@ -234,16 +277,22 @@ def gptq_qk_norm_rope(q, k, positions, rope: Rope, q_weight=None, k_weight=None,
     like = q if q is not None else k
     if like is None:
         raise ValueError("q or k must be given")
-    q_out, cq = _side("q", q, q_weight, q_out, stream)
-    k_out, ck = _side("k", k, k_weight, k_out, stream)
+    device, raw = _where(like, stream)
+    if raw is None:
+        with _g._torch().cuda.device(device):
+            return gptq_qk_norm_rope(q, k, positions, rope, q_weight, k_weight, q_out, k_out, d_status, stream)
+    q_out, cq = _side("q", q, q_weight, q_out, device, stream)
+    k_out, ck = _side("k", k, k_weight, k_out, device, stream)
     tokens, _, dim = like.shape
     if k is not None and (k.shape[0] != tokens or k.shape[2] != dim or k.dtype != like.dtype):
         raise ValueError("q and k must have the same tokens, dim and dtype")
     if positions is not None:
-        _int32("positions", positions, (tokens,))
+        _int32("positions", positions, device, (tokens,))
+    if rope.device != device and rope.device is not None:
+        raise _apart(rope, device)
     st = _g.lib().gptq_qk_norm_rope(cq, ck, _g._dtype_code(like), tokens, dim,
-                                    None if positions is None else positions.data_ptr(), rope.c, _status(d_status),
-                                    _raw_stream(stream, like))
+                                    None if positions is None else positions.data_ptr(),
+                                    rope.c, None if d_status is None else _status(d_status, device), raw)
     if st:
         raise _g.GptqError(st, "gptq_qk_norm_rope")
     return q_out, k_out
@@ -253,20 +302,20 @@ def gptq_qk_norm_rope_backward_workspace_bytes(tokens: int, dim: int, q_heads: i
     return int(_g.lib().gptq_qk_norm_rope_backward_workspace_bytes(tokens, dim, q_heads, k_heads))
 
 
-def _grad_side(name, dy, x, weight, stream):
+def _grad_side(name, dy, x, weight, device, stream):
     if dy is None:
         return None, None, None
-    sg = _heads("d" + name, dy)
+    sg = _heads("d" + name, dy, device)
     sx = (0, 0)
     if weight is not None:
         if x is None:
             raise ValueError(f"{name} is needed with its weight")
-        sx = _heads(name, x, dy.dtype, dy.shape)
+        sx = _heads(name, x, device, dy.dtype, dy.shape)
     dx = _empty_as(dy, stream)
     dw = None if weight is None else _empty_as(weight, stream, _g._torch().float32)
     sd = dx.stride()
     return dx, dw, gptq_heads_grad(dy.data_ptr(), sg[0], sg[1], None if weight is None else x.data_ptr(), sx[0], sx[1],
-                                   dx.data_ptr(), sd[0], sd[1], _weight(name + "_weight", weight, dy),
+                                   dx.data_ptr(), sd[0], sd[1], _weight(name + "_weight", weight, dy, device),
                                    None if dw is None else dw.data_ptr(), dy.shape[1])
 
 
@@ -277,22 +326,29 @@ def gptq_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, rope: Rope, q_we
     like = dq_out if dq_out is not None else dk_out
     if like is None:
         raise ValueError("dq_out or dk_out must be given")
-    dq, dqw, cq = _grad_side("q", dq_out, q, q_weight, stream)
-    dk, dkw, ck = _grad_side("k", dk_out, k, k_weight, stream)
+    device, raw = _where(like, stream)
+    if raw is None:
+        with _g._torch().cuda.device(device):
+            return gptq_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, rope, q_weight, k_weight, workspace,
+                                              d_status, stream)
+    dq, dqw, cq = _grad_side("q", dq_out, q, q_weight, device, stream)
+    dk, dkw, ck = _grad_side("k", dk_out, k, k_weight, device, stream)
     tokens, _, dim = like.shape
     if dk_out is not None and (dk_out.shape[0] != tokens or dk_out.shape[2] != dim or dk_out.dtype != like.dtype):
         raise ValueError("dq_out and dk_out must have the same tokens, dim and dtype")
     if positions is not None:
-        _int32("positions", positions, (tokens,))
+        _int32("positions", positions, device, (tokens,))
     if workspace is None and (dqw is not None or dkw is not None):
         need = gptq_qk_norm_rope_backward_workspace_bytes(tokens, dim, 0 if dq is None else dq.shape[1],
                                                           0 if dk is None else dk.shape[1])
         workspace = _g._workspace(need, like, stream)
+    if rope.device != device and rope.device is not None:
+        raise _apart(rope, device)
+    wp, wn = (None, 0) if workspace is None else _given("workspace", workspace, device)
     st = _g.lib().gptq_qk_norm_rope_backward(cq, ck, _g._dtype_code(like), tokens, dim,
-                                             None if positions is None else positions.data_ptr(), rope.c,
-                                             None if workspace is None else workspace.data_ptr(),
-                                             0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                             _status(d_status), _raw_stream(stream, like))
+                                             None if positions is None else positions.data_ptr(),
+                                             rope.c, wp, wn,
+                                             None if d_status is None else _status(d_status, device), raw)
     if st:
         raise _g.GptqError(st, "gptq_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
@@ -302,12 +358,20 @@ def gptq_kv_append(cache: KVCache, batch: KVBatch, k, v, rope: Rope = None, k_we
                    stream=None):
     """Stores the batch's new tokens: k, v [total, kv_heads, dim] (bf16 or fp32), k through the norm
     (k_weight) and rotation (rope) at its place in the sequence."""
+    device, raw = _where(k, stream)
+    if raw is None:
+        with _g._torch().cuda.device(device):
+            return gptq_kv_append(cache, batch, k, v, rope, k_weight, d_status, stream)
     _check_plan(cache, batch)
-    sk = _heads("k", k, None, (batch.total, cache.kv_heads, cache.dim))
-    sv = _heads("v", v, k.dtype, k.shape)
+    sk = _heads("k", k, device, None, (batch.total, cache.kv_heads, cache.dim))
+    sv = _heads("v", v, device, k.dtype, k.shape)
+    for h in (cache, batch) if rope is None or rope.device is None else (cache, batch, rope):
+        if h.device != device:
+            raise _apart(h, device)
     st = _g.lib().gptq_kv_append(cache.c, batch.c, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1],
-                                 _g._dtype_code(k), _weight("k_weight", k_weight, k),
-                                 None if rope is None else rope.c, _status(d_status), _raw_stream(stream, k))
+                                 _g._dtype_code(k), _weight("k_weight", k_weight, k, device),
+                                 None if rope is None else rope.c,
+                                 None if d_status is None else _status(d_status, device), raw)
     if st:
         raise _g.GptqError(st, "gptq_kv_append")
 
@@ -315,6 +379,10 @@ def gptq_kv_append(cache: KVCache, batch: KVBatch, k, v, rope: Rope = None, k_we
 def gptq_kv_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=None, d_status=None, stream=None):
     """(k, v) [total, kv_heads, dim] of the batch's new tokens out of the cache, bf16 unless `dtype`
     or the given outputs say fp32."""
+    device, raw = _where(cache.k_codes, stream)
+    if raw is None:
+        with _g._torch().cuda.device(device):
+            return gptq_kv_read(cache, batch, dtype, k_out, v_out, d_status, stream)
     _check_plan(cache, batch)
     torch = _g._torch()
     shape = (batch.total, cache.kv_heads, cache.dim)
@@ -326,13 +394,15 @@ def gptq_kv_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=N
         v_out = _empty(shape, cache.k_codes, stream, dtype)
     sk = sv = (0, 0)
     if k_out is not None:
-        sk = _heads("k_out", k_out, dtype, shape)
+        sk = _heads("k_out", k_out, device, dtype, shape)
     if v_out is not None:
-        sv = _heads("v_out", v_out, dtype, shape)
+        sv = _heads("v_out", v_out, device, dtype, shape)
     like = k_out if k_out is not None else v_out
+    if batch.device != device:
+        raise _apart(batch, device)
     st = _g.lib().gptq_kv_read(cache.c, batch.c, None if k_out is None else k_out.data_ptr(), sk[0], sk[1],
                                None if v_out is None else v_out.data_ptr(), sv[0], sv[1], _g._dtype_code(like),
-                               _status(d_status), _raw_stream(stream, like))
+                               None if d_status is None else _status(d_status, device), raw)
     if st:
         raise _g.GptqError(st, "gptq_kv_read")
     return k_out, v_out
@@ -350,9 +420,14 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
     """Attention of the batch's new tokens q [total, q_heads, dim] (bf16 or fp32) over the cache.
     sm_scale: dim^-1/2 unless given.  Returns out, or (out, lse) when lse [total, q_heads] (fp32)
     is given or wanted.  Rows that no sequence owns are left as they are."""
+    device, raw = _where(q, stream)
+    if raw is None:
+        with _g._torch().cuda.device(device):
+            return gptq_kv_attention(q, cache, batch, sm_scale, causal, window, out, lse, want_lse, workspace, d_status,
+                                     stream)
     _check_plan(cache, batch)
     torch = _g._torch()
-    sq = _heads("q", q)
+    sq = _heads("q", q, device)
     total, heads, dim = q.shape
     if total != batch.total or dim != cache.dim:
         raise ValueError("shape mismatch")
@@ -360,25 +435,27 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
         out = _empty_as(q, stream)
         so = out.stride()
     else:
-        so = _heads("out", out, q.dtype, q.shape)
+        so = _heads("out", out, device, q.dtype, q.shape)
     if lse is None:
         if want_lse:
             lse = _empty((total, heads), q, stream, torch.float32)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (total, heads) or not lse.is_cuda or \
-            not lse.is_contiguous():
+    elif lse.get_device() != device:
+        raise _elsewhere("lse", lse, device)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (total, heads) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 [total, q_heads] device tensor")
     a = gptq_attention(heads, 1.0 / math.sqrt(dim) if sm_scale is None else sm_scale, int(causal), window)
     dt = _g._dtype_code(q)
+    if cache.device != device or batch.device != device:
+        raise _apart(cache if cache.device != device else batch, device)
     L = _g.lib()
     if workspace is None:
         need = L.gptq_kv_attention_workspace_bytes(cache.c, batch.c, dt, a)
         if need:
             workspace = _g._workspace(need, q, stream)
+    wp, wn = (None, 0) if workspace is None else _given("workspace", workspace, device)
     st = L.gptq_kv_attention(cache.c, batch.c, a, q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0], so[1],
-                             None if lse is None else lse.data_ptr(), dt,
-                             None if workspace is None else workspace.data_ptr(),
-                             0 if workspace is None else workspace.numel() * workspace.element_size(),
-                             _status(d_status), _raw_stream(stream, q))
+                             None if lse is None else lse.data_ptr(), dt, wp, wn,
+                             None if d_status is None else _status(d_status, device), raw)
     if st:
         raise _g.GptqError(st, "gptq_kv_attention")
     return out if lse is None else (out, lse)
