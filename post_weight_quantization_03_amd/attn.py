@@ -6,6 +6,10 @@ the C struct built from them once; keep them between calls.  The functions carry
 names, marshal arguments, and raise ``GptqError`` on a non-zero status.  Index data on
 the device (positions, lengths, tables) is checked by the kernels: pass ``d_status``, a
 zeroed device int32 tensor, to see whether any was out of range.
+
+A call is made on the device of its tensors, and a call on another ``stream`` allocates what it
+needs from that stream.  gptq_qk_norm_rope is recorded by autograd; the cache's operators are for
+serving and are not.
 """
 
 from __future__ import annotations
@@ -269,14 +273,52 @@ def _side(name, x, weight, out, device, stream):
                            _weight(name + "_weight", weight, x, device), x.shape[1])
 
 
+_recorded = None
+
+
+def _autograd():
+    """gptq_qk_norm_rope as a function of q, k and the weights that autograd records."""
+    global _recorded
+    if _recorded is None:
+        torch = _g._torch()
+
+        class NormRope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, q_weight, k_weight, positions, rope, d_status):
+                ctx.save_for_backward(q, k, q_weight, k_weight, positions)
+                ctx.rope = rope
+                return gptq_qk_norm_rope(q, k, positions, rope, q_weight, k_weight, d_status=d_status)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dq_out, dk_out):
+                q, k, q_weight, k_weight, positions = ctx.saved_tensors
+                # a gradient may come broadcast, with any strides
+                dy = [d if d is None or d.stride(2) == 1 else d.contiguous() for d in (dq_out, dk_out)]
+                dq, dk, dqw, dkw = gptq_qk_norm_rope_backward(*dy, q, k, positions, ctx.rope, q_weight, k_weight)
+                return (dq, dk, None if dqw is None else dqw.to(q_weight.dtype),
+                        None if dkw is None else dkw.to(k_weight.dtype), None, None, None)
+
+        _recorded = NormRope
+    return _recorded
+
+
 def gptq_qk_norm_rope(q, k, positions, rope: Rope, q_weight=None, k_weight=None, q_out=None, k_out=None,
                       d_status=None, stream=None):
     """(q_out, k_out): RMS norm (where a weight [dim] is given) and rotation of every head of
     q and k [tokens, heads, dim] (bf16 or fp32) at positions [tokens] (int32).  q or k may be None;
-    q_out may be q."""
+    q_out may be q.  Where autograd records and q, k or a weight requires gradients, the outputs carry
+    them (weights' gradients rounded to the weight's type); q_out, k_out and stream are then refused."""
     like = q if q is not None else k
     if like is None:
         raise ValueError("q or k must be given")
+    if _g._torch().is_grad_enabled() and (like.requires_grad or k is not None and k.requires_grad or
+                                          q_weight is not None and q_weight.requires_grad or
+                                          k_weight is not None and k_weight.requires_grad):
+        if q_out is not None or k_out is not None or stream is not None:
+            raise ValueError("gradients are recorded for new outputs on the current stream only (torch.no_grad() "
+                             "calls without them)")
+        return _autograd().apply(q, k, q_weight, k_weight, positions, rope, d_status)
     device, raw = _where(like, stream)
     if raw is None:
         with _g._torch().cuda.device(device):
