@@ -83,14 +83,14 @@ class AttentionBlock:
                 "attended": torch.empty((rows, self.q_heads, self.dim), dtype=t, device=self.device),
                 "y": torch.empty((rows, self.hidden), dtype=t, device=self.device),
                 "positions": torch.empty(rows, dtype=torch.int32, device=self.device),
-                "offsets": torch.arange(new, dtype=torch.int32, device=self.device),
+                "offsets": torch.arange(-new, 0, dtype=torch.int32, device=self.device),  # from a sequence's end
                 "workspace": torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)}
 
     def step(self, x, b):
         """Output [rows, hidden] of the block for the next tokens x [rows, hidden] of every sequence."""
         rows, new = x.shape[0], b["new"]
         self.kv_len += new
-        b["positions"].view(-1, new).copy_((self.kv_len - new)[:, None] + b["offsets"])
+        torch.add(self.kv_len[:, None], b["offsets"], out=b["positions"].view(-1, new))
         q, k, v = b["qkv"].split([self.q_heads, self.kv_heads, self.kv_heads], 1)
         self.qkv(x, b["qkv"].view(rows, -1), b["workspace"])
         g.gptq_qk_norm_rope(q, None, b["positions"], self.rope, self.q_weight, q_out=q)
