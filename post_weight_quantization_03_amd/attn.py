@@ -82,18 +82,16 @@ def _elsewhere(name, t, device):
     return ValueError(f"{name} is on device {t.get_device()}, the call on {device}: a call's tensors are on one device")
 
 
-def _where(t, stream):
-    """The device of a call on t, and the HIP stream of `stream` or the device's current one (None: the device is
-    not the current one)."""
-    C = _g._torch()._C
-    d = t.get_device()
+def _raw_stream(torch, d, stream):
+    """The HIP stream of `stream`, or of device d's current one, for a call on device d (None: d is not the current
+    device)."""
     if d < 0:
         raise ValueError("the tensors must be device tensors")
     if stream is not None and stream.device_index != d:
         raise ValueError(f"the stream is on device {stream.device_index}, the call on {d}: they are on one device")
-    if d != C._cuda_getDevice():
-        return d, None
-    return d, C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+    if d != torch._C._cuda_getDevice():
+        return None
+    return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
 
 
 def _int32(name, t, device, shape=None):
@@ -144,8 +142,9 @@ def _given(name, t, device):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _apart(h, device):
+def _apart(device, *handles):
     """The error of a handle whose tensors are not on the call's device."""
+    h = next(h for h in handles if h.device != device)
     return ValueError(f"the {type(h).__name__} is on device {h.device}, the call on {device}: a call's tensors are on "
                       "one device")
 
@@ -312,16 +311,18 @@ def gptq_qk_norm_rope(q, k, positions, rope: Rope, q_weight=None, k_weight=None,
     like = q if q is not None else k
     if like is None:
         raise ValueError("q or k must be given")
-    if _g._torch().is_grad_enabled() and (like.requires_grad or k is not None and k.requires_grad or
-                                          q_weight is not None and q_weight.requires_grad or
-                                          k_weight is not None and k_weight.requires_grad):
+    torch = _g._torch()
+    if torch.is_grad_enabled() and (like.requires_grad or k is not None and k.requires_grad or
+                                    q_weight is not None and q_weight.requires_grad or
+                                    k_weight is not None and k_weight.requires_grad):
         if q_out is not None or k_out is not None or stream is not None:
             raise ValueError("gradients are recorded for new outputs on the current stream only (torch.no_grad() "
                              "calls without them)")
         return _autograd().apply(q, k, q_weight, k_weight, positions, rope, d_status)
-    device, raw = _where(like, stream)
+    device = like.get_device()
+    raw = _raw_stream(torch, device, stream)
     if raw is None:
-        with _g._torch().cuda.device(device):
+        with torch.cuda.device(device):
             return gptq_qk_norm_rope(q, k, positions, rope, q_weight, k_weight, q_out, k_out, d_status, stream)
     q_out, cq = _side("q", q, q_weight, q_out, device, stream)
     k_out, ck = _side("k", k, k_weight, k_out, device, stream)
@@ -331,7 +332,7 @@ def gptq_qk_norm_rope(q, k, positions, rope: Rope, q_weight=None, k_weight=None,
     if positions is not None:
         _int32("positions", positions, device, (tokens,))
     if rope.device != device and rope.device is not None:
-        raise _apart(rope, device)
+        raise _apart(device, rope)
     st = _g.lib().gptq_qk_norm_rope(cq, ck, _g._dtype_code(like), tokens, dim,
                                     None if positions is None else positions.data_ptr(),
                                     rope.c, None if d_status is None else _status(d_status, device), raw)
@@ -368,9 +369,11 @@ def gptq_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, rope: Rope, q_we
     like = dq_out if dq_out is not None else dk_out
     if like is None:
         raise ValueError("dq_out or dk_out must be given")
-    device, raw = _where(like, stream)
+    torch = _g._torch()
+    device = like.get_device()
+    raw = _raw_stream(torch, device, stream)
     if raw is None:
-        with _g._torch().cuda.device(device):
+        with torch.cuda.device(device):
             return gptq_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, rope, q_weight, k_weight, workspace,
                                               d_status, stream)
     dq, dqw, cq = _grad_side("q", dq_out, q, q_weight, device, stream)
@@ -385,7 +388,7 @@ def gptq_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, rope: Rope, q_we
                                                           0 if dk is None else dk.shape[1])
         workspace = _g._workspace(need, like, stream)
     if rope.device != device and rope.device is not None:
-        raise _apart(rope, device)
+        raise _apart(device, rope)
     wp, wn = (None, 0) if workspace is None else _given("workspace", workspace, device)
     st = _g.lib().gptq_qk_norm_rope_backward(cq, ck, _g._dtype_code(like), tokens, dim,
                                              None if positions is None else positions.data_ptr(),
@@ -400,16 +403,19 @@ def gptq_kv_append(cache: KVCache, batch: KVBatch, k, v, rope: Rope = None, k_we
                    stream=None):
     """Stores the batch's new tokens: k, v [total, kv_heads, dim] (bf16 or fp32), k through the norm
     (k_weight) and rotation (rope) at its place in the sequence."""
-    device, raw = _where(k, stream)
+    torch = _g._torch()
+    device = k.get_device()
+    raw = _raw_stream(torch, device, stream)
     if raw is None:
-        with _g._torch().cuda.device(device):
+        with torch.cuda.device(device):
             return gptq_kv_append(cache, batch, k, v, rope, k_weight, d_status, stream)
     _check_plan(cache, batch)
     sk = _heads("k", k, device, None, (batch.total, cache.kv_heads, cache.dim))
     sv = _heads("v", v, device, k.dtype, k.shape)
-    for h in (cache, batch) if rope is None or rope.device is None else (cache, batch, rope):
-        if h.device != device:
-            raise _apart(h, device)
+    if cache.device != device or batch.device != device:
+        raise _apart(device, cache, batch)
+    if rope is not None and rope.device != device and rope.device is not None:
+        raise _apart(device, rope)
     st = _g.lib().gptq_kv_append(cache.c, batch.c, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1],
                                  _g._dtype_code(k), _weight("k_weight", k_weight, k, device),
                                  None if rope is None else rope.c,
@@ -421,12 +427,13 @@ def gptq_kv_append(cache: KVCache, batch: KVBatch, k, v, rope: Rope = None, k_we
 def gptq_kv_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=None, d_status=None, stream=None):
     """(k, v) [total, kv_heads, dim] of the batch's new tokens out of the cache, bf16 unless `dtype`
     or the given outputs say fp32."""
-    device, raw = _where(cache.k_codes, stream)
+    torch = _g._torch()
+    device = cache.device
+    raw = _raw_stream(torch, device, stream)
     if raw is None:
-        with _g._torch().cuda.device(device):
+        with torch.cuda.device(device):
             return gptq_kv_read(cache, batch, dtype, k_out, v_out, d_status, stream)
     _check_plan(cache, batch)
-    torch = _g._torch()
     shape = (batch.total, cache.kv_heads, cache.dim)
     given = k_out if k_out is not None else v_out
     if dtype is None:
@@ -441,7 +448,7 @@ def gptq_kv_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=N
         sv = _heads("v_out", v_out, device, dtype, shape)
     like = k_out if k_out is not None else v_out
     if batch.device != device:
-        raise _apart(batch, device)
+        raise _apart(device, batch)
     st = _g.lib().gptq_kv_read(cache.c, batch.c, None if k_out is None else k_out.data_ptr(), sk[0], sk[1],
                                None if v_out is None else v_out.data_ptr(), sv[0], sv[1], _g._dtype_code(like),
                                None if d_status is None else _status(d_status, device), raw)
@@ -462,13 +469,14 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
     """Attention of the batch's new tokens q [total, q_heads, dim] (bf16 or fp32) over the cache.
     sm_scale: dim^-1/2 unless given.  Returns out, or (out, lse) when lse [total, q_heads] (fp32)
     is given or wanted.  Rows that no sequence owns are left as they are."""
-    device, raw = _where(q, stream)
+    torch = _g._torch()
+    device = q.get_device()
+    raw = _raw_stream(torch, device, stream)
     if raw is None:
-        with _g._torch().cuda.device(device):
+        with torch.cuda.device(device):
             return gptq_kv_attention(q, cache, batch, sm_scale, causal, window, out, lse, want_lse, workspace, d_status,
                                      stream)
     _check_plan(cache, batch)
-    torch = _g._torch()
     sq = _heads("q", q, device)
     total, heads, dim = q.shape
     if total != batch.total or dim != cache.dim:
@@ -488,7 +496,7 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
     a = gptq_attention(heads, 1.0 / math.sqrt(dim) if sm_scale is None else sm_scale, int(causal), window)
     dt = _g._dtype_code(q)
     if cache.device != device or batch.device != device:
-        raise _apart(cache if cache.device != device else batch, device)
+        raise _apart(device, cache, batch)
     L = _g.lib()
     if workspace is None:
         need = L.gptq_kv_attention_workspace_bytes(cache.c, batch.c, dt, a)
