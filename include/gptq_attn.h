@@ -71,8 +71,9 @@ int gptq_qk_norm_rope(const gptq_heads* q, const gptq_heads* k, gptq_dtype dtype
 
 /* Gradients: dx of type dtype from dy and the forward's x, and, where weight is
  * given, dweight (fp32 [dim], written) summed over tokens and heads in a fixed
- * order (bit-reproducible); heads 0: dweight := 0, the other pointers may be NULL.  weight NULL: dx is dy rotated back and x, dweight
- * are not used (may be NULL).  dx may be dy with the same strides. */
+ * order (bit-reproducible); heads 0: dweight := 0, the other pointers may be NULL.
+ * weight NULL: dx is dy rotated back and x, dweight are not used (may be NULL).
+ * dx may be dy with the same strides. */
 typedef struct {
   const void* dy;
   int64_t dy_token, dy_head;

@@ -24,8 +24,16 @@ int64_t product(int64_t a, int64_t b) { return a != 0 && b > INT64_MAX / a ? INT
 //                  128       292 / 523 / 265 / 235    89 / 124 / 89 / 76    33 / 46 / 38 / 35
 //   dim 64 bf16:    64        88 / 68 / 97 / 183      29 / 31 / 50 / 82     16 / 17 / 19 / 23
 //                  800       821 / 822 / 386 / 471   224 / 226 / 117 / 155  83 / 82 / 57 / 69
-// fp32 keeps two parts of queries and weights in registers: its tiles of 32 rows and its 4 waves of 32
-// spill.  dim 256 fits 16 rows, or 4 waves of 32.
+//   dim 256, 4 key heads, tiles of 16 / 128 rows:
+//           bf16:  64 rows  167 / 174     66 / 78     34 / 39
+//                  80       251 / 176     88 / 79     45 / 40
+//                 128       315 / 155     98 / 73     46 / 41
+//           fp32:  64       159 / 444     64 / 141    35 / 56
+//                 128       297 / 434     95 / 139    46 / 59    four prompts of 1024 tokens 277 / 209
+// fp32 keeps two parts of queries and weights in registers: at dim 128 its tiles of 32 rows and its 4 waves of
+// 32 spill, and so do forms that are kept, by bytes a lane: 8 waves of dim 128 in fp32 44, 4 waves of dim 128 in
+// bf16 8, of dim 256 112 in bf16 and 440 in fp32.  dim 256 fits 16 rows, or 4 waves of 32; in fp32 its rule is bf16's, which
+// gains in several short prompts and costs other calls a fifth to a half.
 int tile_rows_for(int64_t rows, int dim, bool bf16) {
   if (dim == 256) return rows <= 64 ? 16 : 128;
   if (rows <= 32) return 16;
@@ -48,14 +56,19 @@ Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const 
   if (p.tile_rows < 128) {
     // Two workgroups of four waves a CU are resident: one round of 512 (one token over 131035 tokens, 8 key
     // heads, chunks of 1024 / 2048 / 2304 / 4096: 60 / 56 / 60 / 88 us).  From 512 on no split is needed for
-    // the chip to be full (64 sequences of up to 8192, 32 heads: 475 us whole, 521 in two).
+    // the chip to be full (64 sequences of up to 8192, 32 heads: 455 to 475 us whole, 521 in two).
     const int64_t want = base >= 512 ? 1 : (512 + base - 1) / base;
     chunk = want == 1 ? span : (span / want + 128) / 256 * 256;
   } else {
     // One workgroup of eight waves a CU.  It starts and ends in the time of 5 tiles of 64 tokens, and its
     // partial results cost a join, so one round of 256 does where chunks stay below 4096 tokens; above, up
     // to three, which even out sequences of different lengths (500 tokens each over 6000 to 12001: 449 us
-    // whole, 382 in two, 350 in three, and 25 for the join).  From 448 on the later workgroups do that.
+    // whole, 382 in two, 350 in three, and 25 for the join).  512 tokens each, in 1 / 2 / 3 parts and by this rule:
+    //   192 workgroups  6000 tokens 183 / 219 / 223, 278    6000 to 12000  323 / 367 / 290, 289
+    //   256             6000        246 / 258 / 258, 279   12000 to 24000  880 / 801 / 739, 739
+    //   448             6000        365 / 446 / 471         6000 to 12000  612 / 645 / 673
+    //   896             6000        750 / 860 / 920         6000 to 12000 1154 / 1304 / 1325
+    // so below 448 it serves unequal sequences, at the cost of equal ones, and from 448 on none is split.
     chunk = base >= 448 ? span : span * base / 256;
     if (base < 448 && chunk > 4096) chunk = span * base / 768 > 4096 ? span * base / 768 : 4096;
   }

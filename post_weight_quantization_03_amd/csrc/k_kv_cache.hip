@@ -17,10 +17,11 @@
 // tokens is read, merged and written, by the one thread that owns it.
 //
 // Three prompts of 8608 tokens in all, 32 heads of 128, bf16 with norm and rotation: 211 MB in 61 to 67 us,
-// 3.2 to 3.5 TB/s of the 4.9 of a copy; the many short-lived workgroups (12672 of 16 KB) bound it, not
-// VALU work or occupancy, and longer-lived ones that take 8 heads in turn are slower (75 us).  One token of
-// each of 64 sequences, 8 heads: 7 us, five dependent accesses.  Reading 214 MB of them back takes 35 us,
-// 6.1 TB/s.
+// 3.2 to 3.5 TB/s of the 4.9 of a copy; in fp32 353 MB in 85 us, 4.1 TB/s.  What bounds it has not been found:
+// fewer VALU instructions (14 to 9 an element) and more or fewer resident waves changed nothing, and of the
+// 12672 workgroups of 16 KB, longer-lived ones that take 8 heads in turn are slower (75 us).  One token of
+// each of 64 sequences, 8 heads: 7 us, five dependent accesses.  Reading 214 MB of them back as bf16 takes 36 us,
+// 6 TB/s.
 #include "attn.h"
 
 namespace gptq {

@@ -19,12 +19,14 @@
 // of a SIMD run half a turn apart, one's products beside the other's softmax, with a
 // barrier where they change over, LDS operands are read 8 products ahead in an order
 // that is written out, and addresses, page look-ups and the scales of 8 tiles at a
-// time stay out of the softmax: 4300 cycles.  What is left is the issue of VALU and
-// matrix instructions, which share a SIMD's port (a product holds it for its operand
-// reads), and the power limit: sustained, the clock is near 2.0 GHz.  A causal prompt of
-// 4096 tokens and 32 heads takes 164 to 180 us, 760 to 840 TFLOP/s of the products that it
-// needs, 0.62 to 0.69 of a large library product's rate; starting and ending a workgroup
-// costs 11 us each, a tenth of it.
+// time stay out of the softmax: 4300 cycles.  Counters over a whole call (3.8e5 cycles):
+// matrix cores busy 37 % of a SIMD's cycles, vector instructions 53 %, some instruction of
+// any kind 75 %, so products and softmax run side by side only in part; what holds the
+// rest has not been traced.  Sustained, the clock is near 2.0 GHz.  A causal prompt of
+// 4096 tokens and 32 heads takes 160 to 164 us (175 to 186 in a loop of its own), 740 to 860 TFLOP/s
+// of the products that it needs, 0.63 to 0.73 of a large library product's rate; starting and
+// ending a workgroup costs 11 us each, a tenth of it.  In fp32, with twice the products and 44 bytes
+// a lane of scratch, 255 to 280 us.
 //
 // The softmax is an fma, an exponential and an addition a score: the key scale
 // times the row's constant is one factor, the maximum is taken before it (it is not
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   const uint32_t page_bytes = (uint32_t)A.cache.kv_heads * (uint32_t)(block * DIM);  // at most 2^31
   const int8_t* k_base = A.cache.k_codes + (int64_t)hk * block * DIM;
   const int8_t* v_base = A.cache.v_codes + (int64_t)hk * block * DIM;
-  // piece i of thread x (with more threads than pieces, two threads do the same one)
+  // piece i of thread x
   auto piece = [&](int x, int i) INLINE { return (x + i * NT) & (PIECES - 1); };
   uint32_t off_k[PER], off_v[PER];
 #pragma unroll

@@ -15,9 +15,10 @@
 // group keeps them in registers over HPT heads of one token; HPT is 4 where
 // that still leaves the chip several waves a SIMD, 1 below.
 //
-// 8195 tokens of 32 and 32 heads of 128 in bf16: 273 MB in 56 us, 4.9 TB/s, the rate of a large copy.
-// Gradients of 4096 tokens, 32 and 8 heads: 128 MB in 29 us (4.4 TB/s) and 3.5 for the weights' sums.  One
-// token: 3 us.
+// 8195 tokens of 32 and 32 heads of 128 in bf16: 273 MB in 56 to 61 us, 4.5 to 4.9 TB/s, the rate of a large
+// copy; in fp32 546 MB in 102 us (5.3 TB/s).  Gradients of 4096 tokens, 32 and 8 heads: 128 MB in 30 us (4.2 TB/s)
+// and 4 for the weights' sums, in fp32 252 MB in 50.  One token: 3 us.  1531 tokens of 14 and 2 heads of 64 in fp32,
+// 19 MB: 10 us and 4, latency: a pass of dependent loads, the groups' sums through LDS, a second launch.
 #include "attn.h"
 
 namespace gptq {
