@@ -25,16 +25,27 @@
 // rest has not been traced.  Sustained, the clock is near 2.0 GHz.  A causal prompt of
 // 4096 tokens and 32 heads takes 160 to 164 us (175 to 186 in a loop of its own), 740 to 860 TFLOP/s
 // of the products that it needs, 0.63 to 0.73 of a large library product's rate; starting and
-// ending a workgroup costs 11 us each, a tenth of it.  In fp32, with twice the products and 44 bytes
-// a lane of scratch, 255 to 280 us.
+// ending a workgroup costs 11 us each, a tenth of it.  In fp32, with twice the products and 68 bytes
+// a lane of scratch, 260 to 280 us.
 //
 // The softmax is an fma, an exponential and an addition a score: the key scale
 // times the row's constant is one factor, the maximum is taken before it (it is not
 // negative), the value scale is added to the exponent (kv_attend.h) and taken back
 // out of the sum once for 16 tokens, and output and sum are rescaled only when a
 // row's maximum has grown by more than 2^7.  Tiles with a value scale that is no power of two, not finite or 2^80
-// below the largest take one more multiplication a score, as do those with masked places.  Sums are of
-// the unrounded weights (of the rounded ones, two at a time, lse lost 1e-4).
+// below the largest take one more multiplication a score, as do those with masked places or scores that
+// may be large.  Sums are of the unrounded weights (of the rounded ones, two at a time, lse lost 1e-4).
+//
+// The reference of a row's weights is an integer m from the largest s + lv on: as a rule differences with it are
+// exact.  The sum of weights is kept to the same m, l = sum 2^(KV_C + s - m): its largest s - m lies between -123 and
+// 100 (and the slack of m), so fp32 has room for it with 2^20 tokens of the least scale, and 2^-24 of it in subnormal
+// numbers.  Both come from one exponential e = 2^(k + s - m), p = e v 2^(P - k), l += e 2^(KV_C - k), with any
+// integer k for which e neither vanishes nor overflows:
+//   k = m less the largest s of the lane's 8 tokens    always does: e is up to 2;
+//   k = P + lv    takes no multiplication where v = 2^lv; it does unless scales lie 2^KV_NEAR apart (e could vanish
+//                 and still count in l).
+// Scores of 2^23 and more leave m no digits for lv: m is then the row's largest score and an integer d beside it, 0
+// else, has the rest.
 #include "kv_attend.h"
 
 // The kernel's parts are lambdas over its registers: a call left in place would put those in memory.
@@ -45,6 +56,9 @@ namespace {
 
 constexpr int PT = 64;                // tokens a tile
 constexpr int SB = 8;                 // tiles whose scales are brought in together
+constexpr float KV_C = -2.0f;
+constexpr float KV_NEAR = 80.0f;
+constexpr float LARGE = 8388608.0f;   // 2^23
 constexpr float P_EXP = 7.0f;         // weights are up to 2^P_EXP in fp16, or
 constexpr float P_SLACK = 7.0f;       // 2^(P_EXP + P_SLACK) while m is up to P_SLACK behind the row's maximum
 
@@ -73,11 +87,12 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   constexpr int KB = PT * KROW, VB = DIM * VROW;
   __shared__ __align__(16) char lds[2 * (KB + VB)];  // [2][KB], [2][VB]
   // Of a tile's four groups of 16 tokens: key scale, the value scale's exponent lv and 2^(KV_C - P_EXP - lv); a bit
-  // for each group of value scale 2^lv, near the largest.  Beside it the value scales, for tiles in which not all
-  // are so.
+  // for each group of value scale 2^lv, near the largest; the largest key scale.  Beside it the value scales, for
+  // tiles in which not all are so.
   struct Scales {
     float ks[4], lv[4], zl[4];
-    int plain, pad[3];
+    int plain;
+    float ks_most, pad[2];
   };
   __shared__ __align__(16) Scales sc[2 * SB];
   __shared__ __align__(16) f32x4 value_scales[2 * SB];
@@ -158,7 +173,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   for (int d = 0; d < ND; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, md = 0.0f, l = 0.0f;
 
   // A thread's pieces of the tiles to come.  The 64 pieces of a wave lie in one group of 16 tokens, for K
   // and for V, so their page is one number a wave, read a tile ahead of the pieces, which thus never wait for
@@ -247,17 +262,22 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     int plain = lv >= lv_most - KV_NEAR && next_vs == ldexpf(1.0f, (int)lv) ? 1 << g : 0;
     plain |= __shfl_xor(plain, 1);
     plain |= __shfl_xor(plain, 2);
+    float ks_most = fmaxf(next_ks, __shfl_xor(next_ks, 1));
+    ks_most = fmaxf(ks_most, __shfl_xor(ks_most, 2));
     if (lane < 4 * SB) {
       sc[at].ks[g] = next_ks;
       sc[at].lv[g] = lv;
       sc[at].zl[g] = ldexpf(1.0f, (int)(KV_C - P_EXP - lv));
       sc[at].plain = plain;
+      sc[at].ks_most = ks_most;
       value_scales[at][g] = next_vs;
     }
   };
 
   f16x8 ph[4], pl[BF16 ? 1 : 4];  // a tile's weights, from its softmax to its output
   Scales S;                       // its scales, read with the last operands of its scores
+  // A score is at most 2^23 times its factor: 2^22 in size where this holds.
+  auto are_small = [&]() INLINE { return S.ks_most * qs < 0.5f; };
   // ANY: with masked places or scales of any kind
   auto softmax = [&]<bool ANY>(int tile, f32x16 (&x)[2]) INLINE {
     f32x4 vs;
@@ -284,19 +304,47 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
       most = fmaxf(most, ANY ? top[g] + S.lv[g] : fmaf(y, f[g], S.lv[g]));
     }
     most = column_max(most);
+    // to a new reference; 2^by in two steps, as l 2^by may be a number where 2^by is none
+    auto turn = [&](float by) INLINE {
+      const float half_way = exp2_fast(0.5f * by);
+      l = l * half_way * half_way;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] *= half_way * half_way;
+    };
+    if (ANY && __any(!are_small() || m >= LARGE)) {
+      float first = fmaxf(m, column_max(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))));
+      const bool large = fabsf(first) >= LARGE && first != -INFINITY;
+      first = large ? first : m;
+      float d = KV_LV_MIN;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) d = fmaxf(d, S.lv[g] - (first - top[g]));
+      d = ceilf(fmaxf(column_max(d), md + (m - first)));
+      d = large ? d : md;
+      turn(large ? (m - first) + (md - d) : 0.0f);
+      m = first, md = d;
+      most = large ? m : most;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        // a score for itself: with m taken off in one step it would not be exact
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float y = x[g >> 1][8 * (g & 1) + i];
+          x[g >> 1][8 * (g & 1) + i] = y == -INFINITY ? y : y * f[g];
+        }
+        f[g] = 1.0f;
+      }
+    }
     if (__any(most > m + P_SLACK)) {
       const float mn = fmaxf(m, ceilf(most));
-      const Decay turn = decay(m - (mn == -INFINITY ? 0.0f : mn));
-      l = l * turn.half * turn.half;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) o[d] *= turn.all;
+      turn(mn > m ? (m - mn) + md : 0.0f);
+      md = mn > m ? 0.0f : md;
       m = mn;
     }
     const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const float k = !ANY ? P_EXP + S.lv[g] : top[g] == -INFINITY ? 0.0f : ceilf(base - top[g]);
-      const float add = k - base;
+      const float k = !ANY ? P_EXP + S.lv[g] : top[g] == -INFINITY ? 0.0f : ceilf(fminf(base - top[g], 1024.0f));
+      const float add = ANY && fabsf(base) >= LARGE ? -top[g] : k - base;
       float p[8], sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -308,7 +356,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += p[i];
       if constexpr (ANY) {
-        const float zp = ldexpf(vs[g], (int)(P_EXP - k));
+        const float zp = ldexpf(vs[g], (int)(P_EXP - md - k));
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = x[g >> 1][8 * (g & 1) + i] == -INFINITY ? 0.0f : p[i] * zp;
       }
@@ -318,7 +366,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
       } else {
         split16(p, ph[g], pl[g]);
       }
-      l = ANY ? l + ldexpf(sum, (int)(KV_C - k)) : fmaf(sum, S.zl[g], l);
+      l = ANY ? l + ldexpf(sum, (int)(KV_C - md - k)) : fmaf(sum, S.zl[g], l);
     }
   };
   // The matrix products of a turn: output of the tile before (PV), scores of this one (QK).  Their LDS operands
@@ -418,7 +466,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
       const int t = t0 + PT * tile;
       // one condition of vector registers, though it is the same in all lanes: as a scalar branch the compiler reads
       // ahead across it, and spills (188 bytes a lane at dim 128)
-      if ((t >= full_lo) & (t + PT <= full_hi) & (S.plain == 15))
+      if ((t >= full_lo) & (t + PT <= full_hi) & (S.plain == 15) & are_small())
         softmax.template operator()<false>(tile, x);
       else
         softmax.template operator()<true>(tile, x);
@@ -457,7 +505,10 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   l = column_sum(l);
   if (r >= rows) return;
   const float inv = l == 0.0f ? 0.0f : exp2_fast(KV_C - P_EXP) / l;
-  const float lse2 = log2_sum(m, l);
+  // the exponent of l is added to m's as the integer that it is
+  const float lse2 = l == 0.0f ? -INFINITY
+                               : m + (md - KV_C + (float)__builtin_amdgcn_frexp_expf(l)) +
+                                     __log2f(__builtin_amdgcn_frexp_mantf(l));
   const int64_t token = s.row + r / group;
   const int head = hk * group + r % group;
   const int64_t at = (token * A.a.q_heads + head) * P.nsplit + split;

@@ -26,8 +26,8 @@
 // With several row tiles each reads the cache: 64 rows over 4 x 30000 tokens, 8 key heads, 246 MB, take 93 us in bf16
 // (one tile of 32 rows twice) and 150 to 155 in fp32 (tiles of 16 rows, four times).
 //
-// Scales: K's multiplies the score (the factor is not negative, so a row's maximum is taken before it), V's goes
-// into the exponent of the weight (kv_attend.h).
+// Scales: K's multiplies the score, V's goes into the exponent of the weight (kv_attend.h), whose reference is kept
+// in two parts, the largest score r and an integer d: scores of any size leave d its digits.
 #include "kv_attend.h"
 
 namespace gptq {
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   constexpr int CW = DIM < 128 ? DIM : 128;  // columns joined at a time
   constexpr int LDO = CW + 4;
   __shared__ __align__(16) float so[KW][16 * LDO];
-  __shared__ float sm[KW][16 * CT], sl[KW][16 * CT];
+  __shared__ float sm[KW][16 * CT], sd[KW][16 * CT], sl[KW][16 * CT];
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n16 = lane & 15, g = lane >> 4;
@@ -143,8 +143,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
     most = fmaxf(most, __shfl_xor(most, 32));
     float up, down;
     row_scale(most, up, down);
-    qs[c] = fabsf(A.a.sm_scale) * 1.44269504088896340736f * down;
-    if (A.a.sm_scale < 0.0f) up = -up;  // the factor of a score is not negative
+    qs[c] = A.a.sm_scale * 1.44269504088896340736f * down;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
 #pragma unroll
@@ -167,10 +166,11 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   }
 
   f32x4 o[CT][ND];
-  float m[CT], l[CT];
+  float m[CT], md[CT], l[CT];  // largest score; integer beside it; sum of 2^(s - m)
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     m[c] = -INFINITY;
+    md[c] = KV_LV_MIN;
     l[c] = 0.0f;
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[c][d] = (f32x4){0, 0, 0, 0};
@@ -205,46 +205,48 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
       const float f = ks_now * qs[c];
-      if (!full) {
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = t + 16 * g + 4 * tt + r;
-            x[c][tt][r] = j >= see[c].lo && j < see[c].hi ? x[c][tt][r] : -INFINITY;
-          }
-      }
       float top = -INFINITY;  // of the 16 scores
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) top = fmaxf(top, x[c][tt][r]);
-      // a masked group stays out whatever its factor is (0, infinite or NaN)
-      top = top == -INFINITY ? top : top * f;
-      float most = top + lv;
-      most = fmaxf(most, __shfl_xor(most, 16));
-      most = fmaxf(most, __shfl_xor(most, 32));
-      const float mn = fmaxf(m[c], ceilf(most));
+        for (int r = 0; r < 4; ++r) {
+          float y = x[c][tt][r] * f;
+          if (!full) {
+            const int j = t + 16 * g + 4 * tt + r;
+            y = j >= see[c].lo && j < see[c].hi ? y : -INFINITY;
+          }
+          x[c][tt][r] = y;
+          top = fmaxf(top, y);
+        }
+      float mn = fmaxf(top, __shfl_xor(top, 16));
+      mn = fmaxf(mn, __shfl_xor(mn, 32));
+      mn = fmaxf(m[c], mn);
       const float base = mn == -INFINITY ? 0.0f : mn;
-      const Decay turn = decay(m[c] - base);
+      const float behind = top == -INFINITY ? 0.0f : base - top, k = ceilf(fminf(behind, 1024.0f));
+      float dn = top == -INFINITY ? KV_LV_MIN : ceilf(lv - behind);
+      dn = fmaxf(dn, __shfl_xor(dn, 16));
+      dn = fmaxf(dn, __shfl_xor(dn, 32));
+      const float risen = m[c] - base;
+      dn = fmaxf(fmaxf(dn, ceilf(md[c] + risen)), KV_LV_MIN);
+      const float turn_l = exp2_fast(risen), turn_o = exp2_fast(risen + (md[c] - dn));
       m[c] = mn;
-      const float k = top == -INFINITY ? 0.0f : ceilf(base - top);
-      const float add = k - base, zp = ldexpf(vs_now, (int)(P_EXP - k));
+      md[c] = dn;
+      // e = 2^(s - top), up to 1; from there to the row's reference by an integer and what is left of it
+      const float from = top == -INFINITY ? 0.0f : top, rest = exp2_fast(k - fminf(behind, 1024.0f));
+      const float zp = ldexpf(vs_now * rest, (int)(P_EXP - dn - k));
       float sum = 0.0f;
       float p[16];
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float y = x[c][tt][r];
-          float e = exp2_fast(fmaf(y, f, add));
-          if (!full) e = y == -INFINITY ? 0.0f : e;  // also where the block's scale of keys is NaN
+          const float y = x[c][tt][r], e = exp2_fast(y - from);
           sum += e;
-          p[4 * tt + r] = full || y != -INFINITY ? e * zp : 0.0f;  // and where that of values is
+          p[4 * tt + r] = full || y != -INFINITY ? e * zp : 0.0f;  // also where the block's scale of values is NaN
         }
-      l[c] = l[c] * turn.half * turn.half + ldexpf(sum, (int)(KV_C - k));
+      l[c] = fmaf(l[c], turn_l, ldexpf(sum * rest, (int)-k));
 #pragma unroll
-      for (int d = 0; d < ND; ++d) o[c][d] *= turn.all;
+      for (int d = 0; d < ND; ++d) o[c][d] *= turn_o;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float q8[8];
@@ -282,7 +284,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   for (int c = 0; c < CT; ++c) {
     l[c] += __shfl_xor(l[c], 16);
     l[c] += __shfl_xor(l[c], 32);
-    if (g == 0) sm[wave][16 * c + n16] = m[c], sl[wave][16 * c + n16] = l[c];
+    if (g == 0) sm[wave][16 * c + n16] = m[c], sd[wave][16 * c + n16] = md[c], sl[wave][16 * c + n16] = l[c];
   }
 #pragma unroll
   for (int c = 0; c < CT; ++c)
@@ -301,33 +303,38 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
 #pragma unroll
         for (int w = 0; w < KW; ++w) mm = fmaxf(mm, sm[w][16 * c + row]);
         const float base = mm == -INFINITY ? 0.0f : mm;
+        float dd = KV_LV_MIN;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) dd = fmaxf(dd, ceilf(sd[w][16 * c + row] + (sm[w][16 * c + row] - base)));
         float sum = 0.0f, y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = 0.0f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const Decay turn = decay(sm[w][16 * c + row] - base);
-          sum += sl[w][16 * c + row] * turn.half * turn.half;
+          const float risen = sm[w][16 * c + row] - base;
+          const float fo = exp2_fast(risen + (sd[w][16 * c + row] - dd));
+          sum = fmaf(sl[w][16 * c + row], exp2_fast(risen), sum);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = fmaf(turn.all, so[w][row * LDO + d + j], y[j]);
+          for (int j = 0; j < 8; ++j) y[j] = fmaf(fo, so[w][row * LDO + d + j], y[j]);
         }
-        const float inv = sum == 0.0f ? 0.0f : exp2_fast(KV_C - P_EXP) / sum;  // a sum of NaN stays NaN
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a sum of NaN stays NaN
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= inv;
-        const float lse2 = log2_sum(mm, sum);
+        for (int j = 0; j < 8; ++j) y[j] = ldexpf(y[j] * inv, (int)(dd - P_EXP));
+        const float lse2 = sum == 0.0f ? -INFINITY : mm + __log2f(sum);
         const int64_t token = s.row + r / group;
         const int head = hk * group + r % group;
+        // lse first: of a condition that ends where the loop does, the compiler has kept the mask for later copies
         if (whole) {
+          if (A.lse && h == 0 && d == 0) A.lse[token * A.a.q_heads + head] = lse2 * 0.69314718055994530942f;
           const int64_t at = token * A.out_token + head * A.out_head + h * CW + d;
           if (A.vec)
             store8<BF16, true>(A.out, at, y);
           else
             store8<BF16, false>(A.out, at, y);
-          if (A.lse && h == 0 && d == 0) A.lse[token * A.a.q_heads + head] = lse2 * 0.69314718055994530942f;
         } else {
           const int64_t at = (token * A.a.q_heads + head) * P.nsplit + split;
-          store8<false, true>(P.out, at * DIM + h * CW + d, y);
           if (h == 0 && d == 0) P.lse2[at] = lse2;
+          store8<false, true>(P.out, at * DIM + h * CW + d, y);
         }
       }
     }

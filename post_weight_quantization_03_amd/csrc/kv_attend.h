@@ -10,19 +10,10 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // A block's value scale v, of size 2^lv, goes into the exponent of its weights: with s the scores (log2) a weight
-// enters the second product, in fp16, as p = v 2^(P + s - m), where m is an integer from the largest s + lv that the
-// row has seen on.  So fp16's range holds what the row's output is made of, whatever the scales of blocks that the
-// row does not see, or sees with no weight to speak of, and differences with m are exact.
-// The sum of weights is kept to the same m, l = sum 2^(KV_C + s - m): its largest s - m lies between -123 and 100 (and
-// the slack of m), so fp32 has room for it with 2^20 tokens of the least scale, and 2^-24 of it in subnormal numbers.
-// Both come from one exponential e = 2^(k + s - m), p = e v 2^(P - k), l += e 2^(KV_C - k), with any integer k
-// for which e neither vanishes nor overflows:
-//   k = m less the largest s of the row's 16 tokens    always does: e is up to 1;
-//   k = P + lv    takes no multiplication where v = 2^lv; it does unless scales lie 2^KV_NEAR apart (e could vanish
-//                 and still count in l).
-constexpr float KV_C = -2.0f;
+// enters the second product, in fp16, as p = v 2^(P + s - ref), where ref goes with the largest s + lv that the row
+// has seen.  So fp16's range holds what the row's output is made of, whatever the scales of blocks that the row does
+// not see, or sees with no weight to speak of.
 constexpr float KV_LV_MIN = -100.0f, KV_LV_MAX = 122.0f;  // what an append writes
-constexpr float KV_NEAR = 80.0f;
 
 // lv; 0 for a scale that is not finite (p is then not finite, l is the scores' as always); the end for a scale of 0
 // or any outside the two.
@@ -102,20 +93,6 @@ __device__ __forceinline__ void row_scale(float most, float& up, float& down) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// x 2^d for d <= 0, in two steps: x 2^d may be a number where 2^d is none.
-struct Decay {
-  float half, all;  // 2^(d / 2), 2^d
-};
-__device__ __forceinline__ Decay decay(float d) {
-  const float h = exp2_fast(0.5f * d);
-  return {h, h * h};
-}
-
-// log2 of a row's sum of weights from m and l; the exponent of l is added to m's as the integer that it is.
-__device__ __forceinline__ float log2_sum(float m, float l) {
-  if (l == 0.0f) return -INFINITY;
-  return (m - KV_C + (float)__builtin_amdgcn_frexp_expf(l)) + __log2f(__builtin_amdgcn_frexp_mantf(l));
-}
 
 // Partial results of split sequences: per row and head, `nsplit` rows of dim fp32
 // (normalised) and their log2 sums.

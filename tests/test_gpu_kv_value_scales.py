@@ -210,3 +210,61 @@ def test_neighbouring_blocks_of_far_sizes(shape, bf16, sizes, qscale):
         v[c.table[0, i]] = 2.0 ** sizes[i % 2]
     scales(c, v=v)
     check(c, [new], 4, bf16, qscale=qscale)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("qscale", [1e4, 1e7, 1e9, 1e13, 1e30])
+def test_scores_far_beyond_the_exponentials_range(shape, bf16, qscale):
+    """Scores of 1e5 to 1e31: the largest alone has weight, and its value is the output.  Where it leads by less than
+    the scores' errors and 64 (a weight of 2^-92) nothing is asked of a row but that it is finite."""
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    new, dim, block = shape
+    say(f"scores of size {qscale}, {shape} bf16={bf16}")
+    rng = np.random.default_rng(79)
+    c = Paged(rng, [new + 130], 2, block, dim)
+    plan, _ = c.plan([new])
+    q = values(rng, (new, 4, dim), bf16, qscale)
+    out, lse = g.gptq_kv_attention(on_device(q, bf16), c.dev, plan, want_lse=True)
+    out, lse = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy()
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    k, v = c.kv(0)
+    asked = 0
+    for i in range(new):
+        for h in range(4):
+            s = k[:131 + i, h // 2] @ q[i, h] / np.sqrt(dim)
+            err = (dim + 8) * 2 * U * (np.abs(k[:131 + i, h // 2]) @ np.abs(q[i, h])).max() / np.sqrt(dim)
+            at = int(s.argmax())
+            if s[at] - np.delete(s, at).max() > 2 * err + 64:
+                want = v[at, h // 2]
+                rest = len(s) * 2.0 ** -92 * np.abs(v).max()
+                assert np.all(np.abs(out[i, h] - want) <= (F + H if bf16 else 2.0 ** -20) * np.abs(want) + rest), (i, h)
+                assert abs(lse[i, h] - s[at]) <= err + 8 * U * abs(s[at])
+                asked += 1
+    assert asked > new
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("window", [0, 40])
+def test_rows_of_large_scores_leave_their_neighbours_alone(shape, bf16, window):
+    """Every third query is 1e9 times as large: the others keep to the bounds of ordinary rows, over blocks of
+    different value scales."""
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    new, dim, block = shape
+    say(f"large scores side by side with ordinary ones, {shape} bf16={bf16} window={window}")
+    rng = np.random.default_rng(80)
+    c = Paged(rng, [new + 130], 2, block, dim)
+    scales(c, v=2.0 ** rng.integers(-20, 11, c.ref.v_scales.shape))
+    plan, _ = c.plan([new])
+    q = values(rng, (new, 4, dim), bf16)
+    ordinary = np.arange(new) % 3 != 1
+    q[~ordinary] *= 2.0 ** 30
+    out, lse = g.gptq_kv_attention(on_device(q, bf16), c.dev, plan, window=window, want_lse=True)
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    want, want_lse, ob, lb, _ = reference(c, 0, q, new + 130, dim ** -0.5, True, window, bf16)
+    close("out", out[ordinary], want[ordinary], ob[ordinary])
+    close("lse", lse[ordinary], want_lse[ordinary], lb[ordinary])
