@@ -20,13 +20,13 @@
 // barrier where they change over, LDS operands are read 8 products ahead in an order
 // that is written out, and addresses, page look-ups and the scales of 8 tiles at a
 // time stay out of the softmax: 4300 cycles.  Counters over a whole call (3.8e5 cycles):
-// matrix cores busy 37 % of a SIMD's cycles, vector instructions 53 %, some instruction of
+// matrix cores busy 36 % of a SIMD's cycles, vector instructions 53 %, some instruction of
 // any kind 75 %, so products and softmax run side by side only in part; what holds the
 // rest has not been traced.  Sustained, the clock is near 2.0 GHz.  A causal prompt of
-// 4096 tokens and 32 heads takes 160 to 164 us (175 to 186 in a loop of its own), 740 to 860 TFLOP/s
+// 4096 tokens and 32 heads takes 160 to 164 us (172 to 186 in a loop of its own), 740 to 860 TFLOP/s
 // of the products that it needs, 0.63 to 0.73 of a large library product's rate; starting and
 // ending a workgroup costs 11 us each, a tenth of it.  In fp32, with twice the products and 68 bytes
-// a lane of scratch, 260 to 280 us.
+// a lane of scratch, 260 to 290 us.
 //
 // The softmax is an fma, an exponential and an addition a score: the key scale
 // times the row's constant is one factor, the maximum is taken before it (it is not

@@ -19,11 +19,11 @@
 // and output; they are joined in LDS at the end, and over the splits of a long
 // sequence by k_kv_join.
 //
-// One token over 64 sequences of 2048 to 8192 tokens, 32 heads of 128: 2.69 GB in 455 us, 5.9 TB/s (a large
+// One token over 64 sequences of 2048 to 8192 tokens, 32 heads of 128: 2.69 GB in 457 us, 5.9 TB/s (a large
 // copy moves 4.9 TB/s, read and written); over 131035 tokens, 8 key heads: 268 MB in 52 us, and 5 for
-// joining 65 splits; over 43 tokens 6.9 us, the latencies of lengths, table, cache and output in turn.  fp32:
-// 456, 54 and 7.1 us.  Three waves a SIMD instead of two spill: 707 us for the first.
-// With several row tiles each reads the cache: 64 rows over 4 x 30000 tokens, 8 key heads, 246 MB, take 93 us in bf16
+// joining 65 splits; over 43 tokens 7 us, the latencies of lengths, table, cache and output in turn.  fp32:
+// 460, 54 to 56 and 7.2 us.  Three waves a SIMD instead of two spill: 707 us for the first.
+// With several row tiles each reads the cache: 64 rows over 4 x 30000 tokens, 8 key heads, 246 MB, take 92 to 95 us in bf16
 // (one tile of 32 rows twice) and 150 to 155 in fp32 (tiles of 16 rows, four times).
 //
 // Scales: K's multiplies the score, V's goes into the exponent of the weight (kv_attend.h), whose reference is kept
