@@ -2,7 +2,8 @@
 
 A thin Python binding over the C ABI of ``libgptq.so`` (declared in
 ``include/gptq.h``; the attention operators, ``include/gptq_attn.h``, are bound
-in ``attn.py`` and exported here).  The functions carry the C names; they only marshal
+in ``attn.py``, the 8-bit integer product, ``include/gptq_int8.h``, in ``int8.py``,
+and exported here).  The functions carry the C names; they only marshal
 arguments -- device pointers and the current HIP stream of PyTorch-ROCm
 tensors -- and raise ``GptqError`` on a non-zero status.  Every step of the
 quantizer runs in the library's HIP kernels; there is no other code path.
@@ -104,6 +105,7 @@ def lib():
     L.gptq_trace_set.argtypes = [vp]
     L.gptq_trace_set.restype = ctypes.c_int
     attn.bind(L)
+    int8.bind(L)
     _lib = L
     return L
 
@@ -401,3 +403,6 @@ from . import attn  # noqa: E402
 from .attn import (KVBatch, KVCache, Rope, gptq_kv_append, gptq_kv_attention,  # noqa: E402,F401
                    gptq_kv_attention_workspace_bytes, gptq_kv_read, gptq_qk_norm_rope, gptq_qk_norm_rope_backward,
                    gptq_qk_norm_rope_backward_workspace_bytes)
+from . import int8  # noqa: E402
+from .int8 import (Tokens, gptq_int8_gemm, gptq_int8_gemm_workspace_bytes, gptq_quantize_tokens,  # noqa: E402,F401
+                   gptq_token_stride)

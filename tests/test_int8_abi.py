@@ -1,0 +1,179 @@
+"""The 8-bit product's C ABI and binding on the host (no GPU): exported symbols, argument errors before
+any device work, tensors of two devices.  Pointers passed here are never dereferenced."""
+
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+
+import post_weight_quantization_03_amd as g
+from post_weight_quantization_03_amd import int8
+from test_binding_devices import Tensor, calls  # noqa: F401
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "gptq_int8.h")
+A = 0x1000  # an aligned address that is not used
+E, U, OK = g.GPTQ_EINVAL, g.GPTQ_EUNSUPPORTED, g.GPTQ_OK
+
+
+def test_every_declared_symbol_is_exported():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"\b(gptq_[a-z0-9_]+)\s*\(", text))
+    assert names == {"gptq_token_stride", "gptq_quantize_tokens", "gptq_int8_gemm", "gptq_int8_gemm_workspace_bytes"}
+    for lib in (g.lib(), ctypes.CDLL(os.path.join(os.path.dirname(g.LIB_PATH), "libgptq_trace.so"))):
+        for n in names:
+            assert hasattr(lib, n), n
+    for n in names:
+        assert callable(getattr(g, n))
+
+
+def test_header_is_plain_c(tmp_path):
+    src = tmp_path / "user.c"
+    src.write_text('#include "gptq_int8.h"\nint main(void) { gptq_tokens t = {0};\n'
+                   '  return gptq_int8_gemm(0, 0, 0, 0, &t, 0, GPTQ_BF16, 0, 0, 0, 0); }\n')
+    r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-fsyntax-only", "-I",
+                        os.path.dirname(HEADER), str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def tokens(codes=A, scales=A, sums=A, n=3, cols=256, stride=256):
+    return int8.gptq_tokens(codes, scales, sums, n, cols, stride)
+
+
+def test_token_stride():
+    f = g.lib().gptq_token_stride
+    for cols, want in ((0, 0), (-5, 0), (1, 128), (128, 128), (129, 256), (65536, 65536), (65537, 0)):
+        assert f(cols) == want
+        if want:
+            assert g.gptq_token_stride(cols) == want
+        else:
+            with pytest.raises(ValueError):
+                g.gptq_token_stride(cols)
+
+
+def quantize(t, X=A, dtype=0, ldx=256):
+    return g.lib().gptq_quantize_tokens(X, dtype, ldx, t, None)
+
+
+def test_quantize_refusals():
+    assert quantize(tokens(n=0), X=None) == OK
+    assert quantize(None) == E
+    assert quantize(tokens(n=-1)) == E
+    assert quantize(tokens(n=(1 << 30) + 1)) == E
+    assert quantize(tokens(cols=0)) == E
+    assert quantize(tokens(cols=65537, stride=66000), ldx=65537) == U
+    assert quantize(tokens(stride=128)) == E
+    assert quantize(tokens(stride=264)) == E
+    assert quantize(tokens(), dtype=2) == E
+    assert quantize(tokens(), ldx=255) == E
+    assert quantize(tokens(), X=None) == E
+    assert quantize(tokens(), X=A + 1) == E
+    assert quantize(tokens(), X=A + 2, dtype=1) == E
+    for bad in (dict(codes=None), dict(codes=A + 8), dict(scales=None), dict(scales=A + 2), dict(sums=None)):
+        assert quantize(tokens(**bad)) == E
+    assert quantize(tokens(n=1 << 24)) == U                       # 256 threads each
+    assert quantize(tokens(n=1 << 22, cols=8193, stride=8320), ldx=8193) == U  # 1024 threads each
+
+
+def gemm(t=None, packed=A, scales=A, zeros=A, rows=64, Y=A, dtype=0, ldy=64, ws=A, ws_bytes=1 << 40):
+    return g.lib().gptq_int8_gemm(packed, scales, zeros, rows, tokens() if t is None else t, Y, dtype, ldy, ws, ws_bytes,
+                                  None)
+
+
+def test_gemm_refusals():
+    assert gemm(t=tokens(n=0)) == OK
+    assert gemm(rows=0) == OK
+    assert gemm(rows=-1) == E
+    assert gemm(rows=(1 << 30) + 1, ldy=1 << 31) == E
+    assert gemm(t=tokens(cols=254)) == E           # not whole words
+    assert gemm(t=tokens(cols=65540, stride=65664)) == U
+    assert gemm(t=tokens(stride=240)) == E
+    assert gemm(dtype=3) == E
+    assert gemm(ldy=63) == E
+    for bad in (dict(packed=None), dict(packed=A + 2), dict(scales=None), dict(scales=A + 1), dict(zeros=None),
+                dict(Y=None), dict(Y=A + 1), dict(Y=A + 2, dtype=1), dict(t=tokens(codes=A + 8)),
+                dict(t=tokens(scales=None)), dict(t=tokens(sums=None))):
+        assert gemm(**bad) == E
+    assert gemm(t=tokens(n=1 << 30), rows=1 << 30, ldy=1 << 30) == U
+
+
+def test_workspace_bytes_of_sizes_out_of_range():
+    f = g.lib().gptq_int8_gemm_workspace_bytes
+    for rows, cols, n in ((0, 128, 1), (-1, 128, 1), (16, 0, 1), (16, 65540, 1), (16, 128, 0), (1 << 31, 128, 1),
+                          (16, 128, 1 << 31)):
+        assert f(rows, cols, n) == 0
+
+
+def test_short_workspace_is_refused():
+    f = g.lib().gptq_int8_gemm_workspace_bytes
+    cases = [(r, c, n) for r in (64, 1000, 4096) for c in (256, 4096, 65536) for n in (1, 40, 200, 1000) if f(r, c, n)]
+    for rows, cols, n in cases:
+        t = tokens(n=n, cols=cols, stride=cols)
+        need = f(rows, cols, n)
+        assert gemm(t=t, rows=rows, ldy=rows, ws_bytes=need - 1) == g.GPTQ_EWORKSPACE
+        assert gemm(t=t, rows=rows, ldy=rows, ws=None, ws_bytes=need) == g.GPTQ_EWORKSPACE
+        assert gemm(t=t, rows=rows, ldy=rows, ws=A + 4, ws_bytes=need) == E
+
+
+def test_binding_refusals():
+    import torch
+    with pytest.raises(ValueError):
+        g.gptq_quantize_tokens(torch.zeros((3, 128)))
+    with pytest.raises(ValueError):
+        g.Tokens.empty(3, 128, "cpu")
+
+
+def arguments(odd=None):
+    import torch
+
+    def t(name, shape, dtype):
+        return Tensor(shape, dtype, 0 if name == odd else 1)
+    return {"X": t("X", (3, 256), torch.float32), "codes": t("codes", (3, 256), torch.int8),
+            "scales": t("scales", (3,), torch.float32), "sums": t("sums", (3,), torch.int32),
+            "packed": WordTensor((16, 64), torch.int32, 0 if odd == "packed" else 1),
+            "w_scales": t("w_scales", (16, 1), torch.float32), "zeros": t("zeros", (16, 1), torch.uint8),
+            "Y": t("Y", (3, 16), torch.bfloat16), "workspace": t("workspace", (64,), torch.uint8)}
+
+
+class WordTensor(Tensor):
+    def element_size(self):
+        return 4
+
+
+def made(a):
+    return g.Tokens(a["codes"], a["scales"], a["sums"], 256)
+
+
+CALLS = {"gptq_quantize_tokens": (("X", "codes", "scales", "sums"), lambda a: g.gptq_quantize_tokens(a["X"], made(a))),
+         "gptq_int8_gemm": (("packed", "w_scales", "zeros", "codes", "Y", "workspace"), lambda a: g.gptq_int8_gemm(
+             a["packed"], a["w_scales"], a["zeros"], made(a), a["Y"], workspace=a["workspace"]))}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_the_call_is_made_on_its_tensors_device(calls, name):  # noqa: F811
+    CALLS[name][1](arguments())
+    assert calls == [(name, 1)]
+
+
+@pytest.mark.parametrize("name,odd", [(n, o) for n in CALLS for o in CALLS[n][0]])
+def test_tensors_of_two_devices_are_refused(calls, name, odd):  # noqa: F811
+    with pytest.raises(ValueError, match="one device"):
+        CALLS[name][1](arguments(odd))
+    assert calls == []
+
+
+def test_shapes_are_checked(calls):  # noqa: F811
+    import torch
+    a = arguments()
+    for bad in (dict(scales=Tensor((15, 1), torch.float32)), dict(zeros=Tensor((16, 2), torch.uint8)),
+                dict(zeros=Tensor((16, 1), torch.int8)), dict(Y=Tensor((3, 15), torch.bfloat16)),
+                dict(Y=Tensor((3, 16), torch.bfloat16), dtype=torch.float32)):
+        args = {"scales": a["w_scales"], "zeros": a["zeros"], "Y": None, "dtype": None, **bad}
+        with pytest.raises(ValueError):
+            g.gptq_int8_gemm(a["packed"], args["scales"], args["zeros"], made(a), args["Y"], dtype=args["dtype"])
+    with pytest.raises(ValueError):
+        g.Tokens(a["codes"], a["scales"], a["sums"], 257)
+    with pytest.raises(ValueError):
+        g.gptq_quantize_tokens(Tensor((4, 256), torch.float32), made(a))
+    assert calls == []
