@@ -1,7 +1,7 @@
 """GPTQ layer quantizer for AMD Instinct MI355X (gfx950).
 
 A thin Python binding over the C ABI of ``libgptq.so`` (declared in
-``include/gptq.h``; the attention operators, ``include/gptq_attn.h``, are bound
+``include/gptq.h``; the attention operators, ``include/gptq_attn.h`` and ``include/gptq_mask.h``, are bound
 in ``attn.py``, the 8-bit integer product, ``include/gptq_int8.h``, in ``int8.py``,
 and exported here).  The functions carry the C names; they only marshal
 arguments -- device pointers and the current HIP stream of PyTorch-ROCm
@@ -400,9 +400,9 @@ def quantize(W, H, params: Params, stream=None, want_what=True):
 
 
 from . import attn  # noqa: E402
-from .attn import (KVBatch, KVCache, Rope, gptq_kv_append, gptq_kv_attention,  # noqa: E402,F401
-                   gptq_kv_attention_workspace_bytes, gptq_kv_read, gptq_qk_norm_rope, gptq_qk_norm_rope_backward,
-                   gptq_qk_norm_rope_backward_workspace_bytes)
+from .attn import (KVBatch, KVCache, KVTree, Rope, gptq_kv_append, gptq_kv_attention,  # noqa: E402,F401
+                   gptq_kv_attention_workspace_bytes, gptq_kv_read, gptq_kv_tree, gptq_qk_norm_rope,
+                   gptq_qk_norm_rope_backward, gptq_qk_norm_rope_backward_workspace_bytes)
 from . import int8  # noqa: E402
 from .int8 import (Tokens, gptq_int8_gemm, gptq_int8_gemm_workspace_bytes, gptq_quantize_tokens,  # noqa: E402,F401
                    gptq_token_stride)

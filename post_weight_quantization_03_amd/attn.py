@@ -1,7 +1,8 @@
-"""The attention operators of libgptq.so (``include/gptq_attn.h``): per-head norm with
-position rotation, the paged 8-bit cache, and attention over it.
+"""The attention operators of libgptq.so (``include/gptq_attn.h``, ``include/gptq_mask.h``): per-head
+norm with position rotation, the paged 8-bit cache, and attention over it, with visible first tokens
+beside a window and with trees of drafted tokens.
 
-``KVCache``, ``KVBatch`` and ``Rope`` hold the tensors a call refers to together with
+``KVCache``, ``KVBatch``, ``KVTree`` and ``Rope`` hold the tensors a call refers to together with
 the C struct built from them once; keep them between calls.  The functions carry the C
 names, marshal arguments, and raise ``GptqError`` on a non-zero status.  Index data on
 the device (positions, lengths, tables) is checked by the kernels: pass ``d_status``, a
@@ -51,8 +52,12 @@ class gptq_attention(ctypes.Structure):
     _fields_ = [("q_heads", _i32), ("sm_scale", _f), ("causal", _i32), ("window", _i64)]
 
 
+class gptq_kv_mask(ctypes.Structure):
+    _fields_ = [("sinks", _i64), ("tree", _vp), ("tree_stride", _i64), ("positions", _vp)]
+
+
 def bind(L):
-    """Argument and result types of the entry points of gptq_attn.h."""
+    """Argument and result types of the entry points of gptq_attn.h and gptq_mask.h."""
     P, ci = ctypes.POINTER, ctypes.c_int
     L.gptq_qk_norm_rope.argtypes = [P(gptq_heads), P(gptq_heads), ci, _i64, _i32, _vp, P(gptq_rope), _vp, _vp]
     L.gptq_qk_norm_rope.restype = ci
@@ -71,6 +76,14 @@ def bind(L):
     L.gptq_kv_attention.argtypes = [P(gptq_kv_cache), P(gptq_kv_batch), P(gptq_attention), _vp, _i64, _i64, _vp,
                                     _i64, _i64, _vp, ci, _vp, _sz, _vp, _vp]
     L.gptq_kv_attention.restype = ci
+    L.gptq_kv_masked_attention_workspace_bytes.argtypes = [P(gptq_kv_cache), P(gptq_kv_batch), ci, P(gptq_attention),
+                                                           P(gptq_kv_mask)]
+    L.gptq_kv_masked_attention_workspace_bytes.restype = _sz
+    L.gptq_kv_masked_attention.argtypes = [P(gptq_kv_cache), P(gptq_kv_batch), P(gptq_attention), P(gptq_kv_mask), _vp,
+                                           _i64, _i64, _vp, _i64, _i64, _vp, ci, _vp, _sz, _vp, _vp]
+    L.gptq_kv_masked_attention.restype = ci
+    L.gptq_kv_tree.argtypes = [P(gptq_kv_batch), _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp]
+    L.gptq_kv_tree.restype = ci
 
 
 # --------------------------------------------------------------------------- helpers
@@ -250,6 +263,35 @@ class KVBatch:
         stride = block_table.stride(0) if batch > 1 else self.blocks
         self.c = gptq_kv_batch(q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), stride, batch, total,
                                max_new, max_kv)
+
+
+class KVTree:
+    """What the new tokens of a batch see of each other: mask int64 [total, words >= ceil(max_new / 64)],
+    bit a % 64 of word a / 64 set in a token's row where it sees its sequence's new token a; positions int32
+    [total].  gptq_kv_tree makes one from parents (and notes the window and sinks it is for); any other
+    mask will do."""
+
+    def __init__(self, positions, mask, window: int = None, sinks: int = None):
+        torch = _g._torch()
+        self.device = _one_device(positions, mask)
+        _int32("positions", positions, self.device, (mask.shape[0],))
+        if mask.dim() != 2 or mask.dtype != torch.int64 or mask.stride(1) != 1 and mask.shape[1] > 1:
+            raise ValueError("mask must be an int64 [total, words] device tensor with unit stride in a row")
+        self.positions, self.mask, self.window, self.sinks = positions, mask, window, sinks
+        self.total, self.words = mask.shape
+        self.stride = mask.stride(0) if self.total > 1 else self.words
+
+    @classmethod
+    def empty(cls, batch: KVBatch):
+        """Room for the positions and masks of a batch."""
+        torch = _g._torch()
+        return cls(batch.kv_len.new_empty((batch.total,)),
+                   batch.kv_len.new_empty((batch.total, -(-batch.max_new // 64)), dtype=torch.int64))
+
+
+def _check_tree(tree, batch):
+    if tree.total != batch.total or 64 * tree.words < batch.max_new:
+        raise ValueError("the tree must have a row for each of the batch's tokens and a bit for each new one")
 
 
 def _check_plan(cache, batch):
@@ -457,25 +499,35 @@ def gptq_kv_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=N
     return k_out, v_out
 
 
+def _mask(sinks, tree):
+    if tree is None:
+        return gptq_kv_mask(sinks, None, 0, None)
+    return gptq_kv_mask(sinks, tree.mask.data_ptr(), tree.stride, tree.positions.data_ptr())
+
+
 def gptq_kv_attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, dtype: int, causal: bool = True,
-                                      window: int = 0) -> int:
-    """Workspace bytes of gptq_kv_attention; dtype: GPTQ_BF16 or GPTQ_F32."""
-    return int(_g.lib().gptq_kv_attention_workspace_bytes(cache.c, batch.c, dtype,
-                                                          gptq_attention(q_heads, 1.0, int(causal), window)))
+                                      window: int = 0, sinks: int = 0) -> int:
+    """Workspace bytes of gptq_kv_attention, with a tree or without; dtype: GPTQ_BF16 or GPTQ_F32."""
+    a = gptq_attention(q_heads, 1.0, int(causal), window)
+    if sinks:
+        return int(_g.lib().gptq_kv_masked_attention_workspace_bytes(cache.c, batch.c, dtype, a, _mask(sinks, None)))
+    return int(_g.lib().gptq_kv_attention_workspace_bytes(cache.c, batch.c, dtype, a))
 
 
 def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: bool = True, window: int = 0,
-                      out=None, lse=None, want_lse: bool = False, workspace=None, d_status=None, stream=None):
+                      out=None, lse=None, want_lse: bool = False, workspace=None, d_status=None, stream=None,
+                      sinks: int = 0, tree: KVTree = None):
     """Attention of the batch's new tokens q [total, q_heads, dim] (bf16 or fp32) over the cache.
-    sm_scale: dim^-1/2 unless given.  Returns out, or (out, lse) when lse [total, q_heads] (fp32)
-    is given or wanted.  Rows that no sequence owns are left as they are."""
+    sm_scale: dim^-1/2 unless given.  sinks: first tokens that the window leaves visible.  tree: the new
+    tokens see those of their masks, and what was before them.  Returns out, or (out, lse) when lse
+    [total, q_heads] (fp32) is given or wanted.  Rows that no sequence owns are left as they are."""
     torch = _g._torch()
     device = q.get_device()
     raw = _raw_stream(torch, device, stream)
     if raw is None:
         with torch.cuda.device(device):
             return gptq_kv_attention(q, cache, batch, sm_scale, causal, window, out, lse, want_lse, workspace, d_status,
-                                     stream)
+                                     stream, sinks, tree)
     _check_plan(cache, batch)
     sq = _heads("q", q, device)
     total, heads, dim = q.shape
@@ -498,14 +550,58 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
     if cache.device != device or batch.device != device:
         raise _apart(device, cache, batch)
     L = _g.lib()
+    mask = None
+    if sinks or tree is not None:
+        if tree is not None:
+            if tree.device != device:
+                raise _apart(device, tree)
+            _check_tree(tree, batch)
+            if (tree.window, tree.sinks) not in ((window, sinks), (None, None)):
+                raise ValueError(f"the tree was made for window {tree.window} and sinks {tree.sinks}")
+        mask = _mask(sinks, tree)
     if workspace is None:
-        need = L.gptq_kv_attention_workspace_bytes(cache.c, batch.c, dt, a)
+        need = (L.gptq_kv_attention_workspace_bytes(cache.c, batch.c, dt, a) if mask is None else
+                L.gptq_kv_masked_attention_workspace_bytes(cache.c, batch.c, dt, a, mask))
         if need:
             workspace = _g._workspace(need, q, stream)
     wp, wn = (None, 0) if workspace is None else _given("workspace", workspace, device)
+    if mask is not None:
+        st = L.gptq_kv_masked_attention(cache.c, batch.c, a, mask, q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0],
+                                        so[1], None if lse is None else lse.data_ptr(), dt, wp, wn,
+                                        None if d_status is None else _status(d_status, device), raw)
+        if st:
+            raise _g.GptqError(st, "gptq_kv_masked_attention")
+        return out if lse is None else (out, lse)
     st = L.gptq_kv_attention(cache.c, batch.c, a, q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0], so[1],
                              None if lse is None else lse.data_ptr(), dt, wp, wn,
                              None if d_status is None else _status(d_status, device), raw)
     if st:
         raise _g.GptqError(st, "gptq_kv_attention")
     return out if lse is None else (out, lse)
+
+
+def gptq_kv_tree(batch: KVBatch, parents, window: int = 0, sinks: int = 0, out: KVTree = None, d_status=None,
+                 stream=None) -> KVTree:
+    """Positions and masks of the batch's new tokens as trees, new ones or `out`: parents int32 [total] holds
+    for each the new token of its sequence that it follows, an earlier one, or -1 for the cache's last token.
+    window and sinks: those of the attention that the tree is for."""
+    torch = _g._torch()
+    device = batch.device
+    raw = _raw_stream(torch, device, stream)
+    if raw is None:
+        with torch.cuda.device(device):
+            return gptq_kv_tree(batch, parents, window, sinks, out, d_status, stream)
+    _int32("parents", parents, device, (batch.total,))
+    if out is None:
+        out = KVTree(_empty((batch.total,), batch.kv_len, stream, torch.int32),
+                     _empty((batch.total, -(-batch.max_new // 64)), batch.kv_len, stream, torch.int64))
+    else:
+        if out.device != device:
+            raise _apart(device, out)
+        _check_tree(out, batch)
+    st = _g.lib().gptq_kv_tree(batch.c, parents.data_ptr(), window, sinks, out.positions.data_ptr(),
+                               out.mask.data_ptr(), out.stride, None if d_status is None else _status(d_status, device), raw)
+    if st:
+        raise _g.GptqError(st, "gptq_kv_tree")
+    out.window, out.sinks = window, sinks
+    return out

@@ -3,6 +3,7 @@
 
 #include "common.h"
 #include "gptq_attn.h"
+#include "gptq_mask.h"
 
 namespace gptq {
 
@@ -68,12 +69,18 @@ struct KvAttention {
   int bf16, vec;
   void* workspace;
   int32_t* d_status;
+  int masked;         // with visible first tokens or a tree; else mask is not looked at
+  gptq_kv_mask mask;  // sinks 0 without a window
 };
 size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool bf16,
-                              const gptq_attention& a);
+                              const gptq_attention& a, int64_t sinks);
 // Whether the call's launches stay below 2^32 threads each.
-bool kv_attention_fits(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool bf16, const gptq_attention& a);
+bool kv_attention_fits(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool bf16, const gptq_attention& a,
+                       int64_t sinks);
 hipError_t kv_attention(const KvAttention& a, hipStream_t stream);
+
+hipError_t kv_tree(const gptq_kv_batch& b, const int32_t* parents, int64_t window, int64_t sinks, int32_t* positions,
+                   uint64_t* tree, int64_t stride, int32_t* d_status, hipStream_t stream);
 
 inline bool kv_block_ok(int32_t block) { return block == 16 || block == 32 || block == 64 || block == 128; }
 inline bool kv_dim_ok(int32_t dim) { return dim == 64 || dim == 128 || dim == 256; }

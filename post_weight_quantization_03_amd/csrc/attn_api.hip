@@ -246,18 +246,44 @@ static gptq_attention limited(const gptq_attention* a, const gptq_kv_batch* batc
   return r;
 }
 
-size_t gptq_kv_attention_workspace_bytes(const gptq_kv_cache* cache, const gptq_kv_batch* batch, gptq_dtype dtype,
-                                         const gptq_attention* a) {
-  if (attention_check(cache, batch, dtype, a) != GPTQ_OK || batch_empty(batch)) return 0;
-  return kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, limited(a, batch));
+static int mask_check(const gptq_kv_batch* batch, const gptq_attention* a, const gptq_kv_mask* m) {
+  if (!m || m->sinks < 0) return GPTQ_EINVAL;
+  if (m->tree && (!a->causal || m->tree_stride < (batch->max_new + 63) / 64 || !stride_ok(m->tree_stride)))
+    return GPTQ_EINVAL;
+  return GPTQ_OK;
 }
 
-int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const gptq_attention* att, const void* q,
-                      int64_t q_token, int64_t q_head, void* out, int64_t out_token, int64_t out_head, float* lse,
-                      gptq_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* d_status,
-                      gptq_stream_t stream) {
-  int st = attention_check(cache, batch, dtype, att);
-  if (st != GPTQ_OK) return st;
+// First tokens that count: none without a window, and no more than a sequence has.
+static int64_t counted_sinks(const gptq_attention& seen, const gptq_kv_batch* batch, const gptq_kv_mask* m) {
+  if (!m || seen.window == 0) return 0;
+  return m->sinks < batch->max_kv ? m->sinks : batch->max_kv;
+}
+
+static size_t workspace_of(const gptq_kv_cache* cache, const gptq_kv_batch* batch, gptq_dtype dtype,
+                           const gptq_attention* a, const gptq_kv_mask* mask) {
+  if (batch_empty(batch)) return 0;
+  const gptq_attention seen = limited(a, batch);
+  return kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, seen, counted_sinks(seen, batch, mask));
+}
+
+size_t gptq_kv_attention_workspace_bytes(const gptq_kv_cache* cache, const gptq_kv_batch* batch, gptq_dtype dtype,
+                                         const gptq_attention* a) {
+  if (attention_check(cache, batch, dtype, a) != GPTQ_OK) return 0;
+  return workspace_of(cache, batch, dtype, a, nullptr);
+}
+
+size_t gptq_kv_masked_attention_workspace_bytes(const gptq_kv_cache* cache, const gptq_kv_batch* batch,
+                                                gptq_dtype dtype, const gptq_attention* a, const gptq_kv_mask* mask) {
+  if (attention_check(cache, batch, dtype, a) != GPTQ_OK || mask_check(batch, a, mask) != GPTQ_OK) return 0;
+  return workspace_of(cache, batch, dtype, a, mask);
+}
+
+// The call behind both entry points; mask NULL: none.
+static int attend(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const gptq_attention* att,
+                  const gptq_kv_mask* mask, const void* q, int64_t q_token, int64_t q_head, void* out,
+                  int64_t out_token, int64_t out_head, float* lse, gptq_dtype dtype, void* workspace,
+                  size_t workspace_bytes, int32_t* d_status, gptq_stream_t stream) {
+  int st;
   if (!stride_ok(q_token) || !stride_ok(q_head) || !stride_ok(out_token) || !stride_ok(out_head) ||
       !aligned(d_status, 4))
     return GPTQ_EINVAL;
@@ -268,8 +294,12 @@ int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, co
   // with no token in any sequence no page exists to be pointed at
   if (batch->max_kv > 0 && (st = cache_pointers(cache)) != GPTQ_OK) return st;
   const gptq_attention seen = limited(att, batch);
-  if (!kv_attention_fits(*cache, *batch, dtype == GPTQ_BF16, seen)) return GPTQ_EUNSUPPORTED;
-  const size_t need = kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, seen);
+  const int64_t sinks = counted_sinks(seen, batch, mask);
+  const bool tree = mask && mask->tree;
+  if (tree && (!aligned(mask->tree, 8) || (seen.window > 0 && (!mask->positions || !aligned(mask->positions, 4)))))
+    return GPTQ_EINVAL;
+  if (!kv_attention_fits(*cache, *batch, dtype == GPTQ_BF16, seen, sinks)) return GPTQ_EUNSUPPORTED;
+  const size_t need = kv_attention_workspace(*cache, *batch, dtype == GPTQ_BF16, seen, sinks);
   if (workspace_bytes < need || (need > 0 && !workspace)) return GPTQ_EWORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return GPTQ_EINVAL;
   KvAttention a{};
@@ -283,7 +313,50 @@ int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, co
   a.vec = vec_ok(q, q_token, q_head, dtype) && vec_ok(out, out_token, out_head, dtype);
   a.workspace = workspace;
   a.d_status = d_status;
+  a.masked = tree || sinks > 0;
+  if (a.masked) a.mask = *mask;
+  a.mask.sinks = sinks;
   return kv_attention(a, (hipStream_t)stream) == hipSuccess ? GPTQ_OK : GPTQ_EHIP;
+}
+
+int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const gptq_attention* att, const void* q,
+                      int64_t q_token, int64_t q_head, void* out, int64_t out_token, int64_t out_head, float* lse,
+                      gptq_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* d_status,
+                      gptq_stream_t stream) {
+  const int st = attention_check(cache, batch, dtype, att);
+  if (st != GPTQ_OK) return st;
+  return attend(cache, batch, att, nullptr, q, q_token, q_head, out, out_token, out_head, lse, dtype, workspace,
+                workspace_bytes, d_status, stream);
+}
+
+int gptq_kv_masked_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const gptq_attention* att,
+                             const gptq_kv_mask* mask, const void* q, int64_t q_token, int64_t q_head, void* out,
+                             int64_t out_token, int64_t out_head, float* lse, gptq_dtype dtype, void* workspace,
+                             size_t workspace_bytes, int32_t* d_status, gptq_stream_t stream) {
+  int st = attention_check(cache, batch, dtype, att);
+  if (st != GPTQ_OK || (st = mask_check(batch, att, mask)) != GPTQ_OK) return st;
+  return attend(cache, batch, att, mask, q, q_token, q_head, out, out_token, out_head, lse, dtype, workspace,
+                workspace_bytes, d_status, stream);
+}
+
+int gptq_kv_tree(const gptq_kv_batch* batch, const int32_t* parents, int64_t window, int64_t sinks,
+                 int32_t* positions, uint64_t* tree, int64_t tree_stride, int32_t* d_status, gptq_stream_t stream) {
+  if (!batch || batch->batch < 0 || batch->batch > MAX_DIM || batch->total < 0 || batch->total > MAX_DIM ||
+      batch->max_new < 0 || batch->max_new > MAX_DIM || batch->max_kv < 0 || batch->max_kv > MAX_DIM)
+    return GPTQ_EINVAL;
+  if (window < 0 || sinks < 0 || tree_stride < (batch->max_new + 63) / 64 || !stride_ok(tree_stride) ||
+      !aligned(d_status, 4))
+    return GPTQ_EINVAL;
+  if (batch_empty(batch)) return GPTQ_OK;
+  if (!batch->q_start || !batch->kv_len || !parents || !positions || !tree || !aligned(batch->q_start, 4) ||
+      !aligned(batch->kv_len, 4) || !aligned(parents, 4) || !aligned(positions, 4) || !aligned(tree, 8) ||
+      parents == positions)
+    return GPTQ_EINVAL;
+  if (batch->batch > MAX_GRID) return GPTQ_EUNSUPPORTED;
+  return kv_tree(*batch, parents, window, sinks, positions, tree, tree_stride, d_status, (hipStream_t)stream) ==
+                 hipSuccess
+             ? GPTQ_OK
+             : GPTQ_EHIP;
 }
 
 }  // extern "C"

@@ -42,7 +42,8 @@ int tile_rows_for(int64_t rows, int dim, bool bf16) {
   return rows <= 128 || dim == 64 ? 128 : 256;
 }
 
-Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const gptq_attention& a) {
+// sinks: first tokens visible beside a window.
+Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const gptq_attention& a, int64_t sinks) {
   const int64_t rows = b.max_new * (a.q_heads / c.kv_heads);
   Plan p;
   p.tile_rows = tile_rows_for(rows, c.dim, bf16);
@@ -50,7 +51,8 @@ Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const 
   p.base = base;
   // tokens a tile may see, with the rounding of its first
   int64_t span = b.max_kv;
-  if (a.window > 0 && a.window + b.max_new < span) span = a.window + b.max_new;
+  const int64_t head = (sinks + 63) / 64 * 64;
+  if (a.window > 0 && head + a.window + b.max_new < span) span = head + a.window + b.max_new;
   span += 63;
   int64_t chunk;
   if (p.tile_rows < 128) {
@@ -81,23 +83,24 @@ Plan make_plan(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const 
 }  // namespace
 
 size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool bf16,
-                              const gptq_attention& a) {
-  const Plan p = make_plan(cache, batch, bf16, a);
+                              const gptq_attention& a, int64_t sinks) {
+  const Plan p = make_plan(cache, batch, bf16, a, sinks);
   if (p.nsplit <= 1) return 0;
   // at most 768 workgroups' splits of 256 rows, times 2^30 tokens: below 2^60
   return (size_t)batch.total * a.q_heads * p.nsplit * (cache.dim + 1) * sizeof(float);
 }
 
-bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const gptq_attention& a) {
+bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, bool bf16, const gptq_attention& a,
+                       int64_t sinks) {
   const int64_t limit = ((int64_t)1 << 32) - 1;
-  const Plan p = make_plan(c, b, bf16, a);
+  const Plan p = make_plan(c, b, bf16, a, sinks);
   // a workgroup a row and head where splits are joined
   if (p.nsplit > 1 && b.batch * b.max_new > limit / 256 / a.q_heads) return false;
   return p.base <= limit / (p.tile_rows == 256 ? 512 : 256) / p.nsplit;
 }
 
 hipError_t kv_attention(const KvAttention& a, hipStream_t stream) {
-  const Plan p = make_plan(a.cache, a.batch, a.bf16, a.a);
+  const Plan p = make_plan(a.cache, a.batch, a.bf16, a.a, a.masked ? a.mask.sinks : 0);
   Partials w{nullptr, nullptr, p.nsplit, p.chunk};
   if (p.nsplit > 1) {
     w.out = static_cast<float*>(a.workspace);

@@ -74,7 +74,7 @@ __device__ __forceinline__ float column_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <int DIM, bool BF16, int NW>
+template <int DIM, bool BF16, int NW, bool MASKED>
 __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAttention A, Partials P, uint32_t pairs,
                                                                            uint32_t row_tiles) {
   constexpr int NK = DIM / 16;         // MFMA steps of the first product
@@ -96,6 +96,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   };
   __shared__ __align__(16) Scales sc[2 * SB];
   __shared__ __align__(16) f32x4 value_scales[2 * SB];
+  __shared__ __align__(16) RowMask masks[MASKED ? 32 * NW : 1];  // only tiles with masked places look at a row's
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 31, half = lane >> 5;
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   const int group = A.a.q_heads / A.cache.kv_heads;
   const int rows = s.n * group, r0 = rt * 32 * NW;
   if (r0 >= rows) return;
-  const Span span = row_span(A, s, r0, 32 * NW, group);
+  const Span span = row_span<MASKED>(A, s, r0, 32 * NW, group);
   const int64_t first = span.begin + split * P.chunk;
   if (split > 0 && first >= span.end) return;
   const bool whole = span.end - span.begin <= P.chunk;
@@ -128,6 +129,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   float qs = 0.0f;
   Sees see = {0, 0};
   int full_lo = 0, full_hi = 0;
+  Full every = {0, 0, 0};
   auto load_queries = [&]() INLINE {
     float x[NK][8];
     float most = 0.0f;
@@ -161,8 +163,14 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
         split16(x[k], qh[k], ql[k]);
       }
     }
-    see = row_sees(A, s, r, group);
-    if (wr0 < rows) {
+    if constexpr (MASKED) {
+      every = full_span(A, s, wr0, (wr0 + 32 < rows ? wr0 + 32 : rows) - 1, group);
+      if (wr0 >= rows) every.hi = 0;
+      if (half == 0) masks[32 * wave + col] = row_mask(A, s, r, group, A.d_status);
+    } else {
+      see = row_sees(A, s, r, group);
+    }
+    if (!MASKED && wr0 < rows) {
       const int last = (wr0 + 32 < rows ? wr0 + 32 : rows) - 1;
       full_lo = row_sees(A, s, last, group).lo, full_hi = row_sees(A, s, wr0, group).hi;
     }
@@ -196,7 +204,11 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     off_k[i] = (uint32_t)((p / (DIM / 16) & (block - 1)) * DIM + p % (DIM / 16) * 16);
     off_v[i] = (uint32_t)((16 * (p / DIM) & (block - 1)) * DIM + p % DIM * 16);
   }
-  auto entry = [&](int tok) INLINE { return table[(tok < t1 ? tok : t1 - 1) >> shift]; };
+  auto actual = [&](int t) INLINE { return MASKED ? span.token(t) : t; };
+  auto entry = [&](int tok) INLINE {
+    const int t = tok < t1 ? tok : t1 - 1;
+    return table[(MASKED ? span.looked_up(t) : t) >> shift];
+  };
   auto checked = [&](int page) INLINE {
     const bool ok = (uint32_t)page < (uint32_t)A.cache.pages;
     bad |= !ok;
@@ -213,7 +225,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const uint32_t page = checked(__builtin_amdgcn_readfirstlane(page_k[i]));
-      kp[i] = *reinterpret_cast<const u32x4v*>(k_base + ((uint64_t)page * page_bytes + (uint32_t)((t & (block - 1)) * DIM)) +
+      kp[i] = *reinterpret_cast<const u32x4v*>(k_base + ((uint64_t)page * page_bytes + (uint32_t)((actual(t) & (block - 1)) * DIM)) +
                                                off_k[i]);
     }
   };
@@ -221,7 +233,7 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const uint32_t page = checked(__builtin_amdgcn_readfirstlane(page_v[i]));
-      vp[i] = *reinterpret_cast<const u32x4v*>(v_base + ((uint64_t)page * page_bytes + (uint32_t)((t & (block - 1)) * DIM)) +
+      vp[i] = *reinterpret_cast<const u32x4v*>(v_base + ((uint64_t)page * page_bytes + (uint32_t)((actual(t) & (block - 1)) * DIM)) +
                                                off_v[i]);
     }
   };
@@ -283,12 +295,17 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
     f32x4 vs;
     if constexpr (ANY) {
       vs = value_scales[tile & (2 * SB - 1)];
+      uint64_t seen = 0;
+      if constexpr (MASKED)
+        seen = row_word(masks[32 * wave + col], s.n, actual(t0 + PT * tile)) >> (4 * half);
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = t0 + PT * tile + 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
-          x[tt][i] = j >= see.lo && j < see.hi ? x[tt][i] : -INFINITY;
+          const bool sees = MASKED ? ((uint32_t)(seen >> (32 * tt)) >> (8 * (i >> 2) + (i & 3)) & 1) != 0
+                                   : j >= see.lo && j < see.hi;
+          x[tt][i] = sees ? x[tt][i] : -INFINITY;
         }
     }
     float f[4], top[4], most = -INFINITY;
@@ -466,7 +483,12 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
       const int t = t0 + PT * tile;
       // one condition of vector registers, though it is the same in all lanes: as a scalar branch the compiler reads
       // ahead across it, and spills (188 bytes a lane at dim 128)
-      if ((t >= full_lo) & (t + PT <= full_hi) & (S.plain == 15) & are_small())
+      if constexpr (MASKED && DIM == 256) {  // with both bodies it spills scalars between them
+        softmax.template operator()<true>(tile, x);
+        return;
+      }
+      const bool all = MASKED ? every.has(actual(t)) : (t >= full_lo) & (t + PT <= full_hi);
+      if (all & (S.plain == 15) & are_small())
         softmax.template operator()<false>(tile, x);
       else
         softmax.template operator()<true>(tile, x);
@@ -549,25 +571,30 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
   }
 }
 
-template <int DIM, bool BF16, int NW>
+template <int DIM, bool BF16, int NW, bool MASKED>
 hipError_t launch(const KvAttention& a, const Partials& p, hipStream_t stream) {
   const int64_t rows = a.batch.max_new * (a.a.q_heads / a.cache.kv_heads);
   const uint32_t tiles = (uint32_t)((rows + 32 * NW - 1) / (32 * NW));
   const uint32_t pairs = (uint32_t)(a.batch.batch * a.cache.kv_heads);
-  k_kv_prompt<DIM, BF16, NW><<<pairs * tiles * (uint32_t)p.nsplit, 64 * NW, 0, stream>>>(a, p, pairs, tiles);
+  k_kv_prompt<DIM, BF16, NW, MASKED><<<pairs * tiles * (uint32_t)p.nsplit, 64 * NW, 0, stream>>>(a, p, pairs, tiles);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t kv_prompt_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
+template <bool MASKED>
+static hipError_t launch_dim(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
   switch (a.cache.dim) {
-    case 64: return a.bf16 ? launch<64, true, 4>(a, p, stream) : launch<64, false, 4>(a, p, stream);
+    case 64: return a.bf16 ? launch<64, true, 4, MASKED>(a, p, stream) : launch<64, false, 4, MASKED>(a, p, stream);
     case 128:
-      if (!a.bf16) return launch<128, false, 8>(a, p, stream);
-      return tile_rows == 256 ? launch<128, true, 8>(a, p, stream) : launch<128, true, 4>(a, p, stream);
-    default: return a.bf16 ? launch<256, true, 4>(a, p, stream) : launch<256, false, 4>(a, p, stream);
+      if (!a.bf16) return launch<128, false, 8, MASKED>(a, p, stream);
+      return tile_rows == 256 ? launch<128, true, 8, MASKED>(a, p, stream) : launch<128, true, 4, MASKED>(a, p, stream);
+    default: return a.bf16 ? launch<256, true, 4, MASKED>(a, p, stream) : launch<256, false, 4, MASKED>(a, p, stream);
   }
+}
+
+hipError_t kv_prompt_launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
+  return a.masked ? launch_dim<true>(a, p, tile_rows, stream) : launch_dim<false>(a, p, tile_rows, stream);
 }
 
 }  // namespace gptq

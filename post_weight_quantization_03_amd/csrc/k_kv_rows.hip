@@ -36,7 +36,7 @@ namespace {
 constexpr int KW = 4;  // waves
 constexpr float P_EXP = 14.0f;  // weights are up to 2^P_EXP in fp16, normal numbers down to 2^-28 of that
 
-template <int DIM, bool BF16, int CT>
+template <int DIM, bool BF16, int CT, bool MASKED>
 __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAttention A, Partials P, uint32_t row_tiles) {
   constexpr int NI = DIM / 64;  // 16-byte K loads a row
   constexpr int NK = DIM / 32;  // MFMA steps of the first product
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   const int group = A.a.q_heads / A.cache.kv_heads;
   const int rows = s.n * group, r0 = rt * 16 * CT;
   if (r0 >= rows) return;
-  const Span span = row_span(A, s, r0, 16 * CT, group);
+  const Span span = row_span<MASKED>(A, s, r0, 16 * CT, group);
   const int64_t first = span.begin + split * P.chunk;
   if (split > 0 && first >= span.end) return;
   const bool whole = span.end - span.begin <= P.chunk;
@@ -82,16 +82,18 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   const int t_stop = (int)stop;
   auto pages = [&](int t) {
     const int tk = t + 16 * gk, tv = t + 16 * g;
-    page_k = table[(tk < t_stop ? tk : t_stop - 1) >> shift];
-    page_v = table[(tv < t_stop ? tv : t_stop - 1) >> shift];
+    const int ck = tk < t_stop ? tk : t_stop - 1, cv = tv < t_stop ? tv : t_stop - 1;
+    page_k = table[(MASKED ? span.looked_up(ck) : ck) >> shift];
+    page_v = table[(MASKED ? span.looked_up(cv) : cv) >> shift];
   };
+  auto actual = [&](int t) { return MASKED ? span.token(t) : t; };
   auto checked = [&](int page) {
     const bool ok = (uint32_t)page < (uint32_t)A.cache.pages;
     bad |= !ok;
     return ok ? (uint32_t)page : 0u;
   };
   auto load_k = [&](int t) {
-    const int8_t* p = k_base + (uint64_t)checked(page_k) * page_bytes + (uint32_t)(((t + 16 * gk) & (block - 1)) * DIM);
+    const int8_t* p = k_base + (uint64_t)checked(page_k) * page_bytes + (uint32_t)(((actual(t) + 16 * gk) & (block - 1)) * DIM);
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   };
   auto load_v = [&](int t) {
     const uint32_t page = checked(page_v);
-    const int8_t* p = v_base + (uint64_t)page * page_bytes + (uint32_t)(((t + 16 * g) & (block - 1)) * DIM);
+    const int8_t* p = v_base + (uint64_t)page * page_bytes + (uint32_t)(((actual(t) + 16 * g) & (block - 1)) * DIM);
 #pragma unroll
     for (int d = 0; d < ND; ++d) vr[d] = *reinterpret_cast<const u32x4v*>(p + 256 * d);
     vs = A.cache.v_scales[(int64_t)page * A.cache.kv_heads + hk];
@@ -119,6 +121,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
   f16x8 qh[CT][NK], ql[CT][BF16 ? 1 : NK];
   float qs[CT];
   Sees see[CT];
+  RowMask mask[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     const int r = r0 + 16 * c + n16;
@@ -155,11 +158,17 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
         split16(x[k], qh[c][k], ql[c][k]);
       }
     }
-    see[c] = row_sees(A, s, r, group);
+    if constexpr (MASKED)
+      mask[c] = row_mask(A, s, r, group, A.d_status);
+    else
+      see[c] = row_sees(A, s, r, group);
   }
   // tokens from full_lo to full_hi are seen by every row of the tile
-  int full_lo, full_hi;
-  {
+  int full_lo = 0, full_hi = 0;
+  Full every;
+  if constexpr (MASKED) {
+    every = full_span(A, s, r0, (r0 + 16 * CT < rows ? r0 + 16 * CT : rows) - 1, group);
+  } else {
     const int last = (r0 + 16 * CT < rows ? r0 + 16 * CT : rows) - 1;
     full_lo = row_sees(A, s, last, group).lo;
     full_hi = row_sees(A, s, r0, group).hi;
@@ -200,11 +209,15 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
     if (tn < t_stop) load_k(tn);
 
     const float lv = value_exponent(vs_now);
-    const bool full = t >= full_lo && t + 64 <= full_hi;
+    const bool full = MASKED ? every.has(actual(t)) : t >= full_lo && t + 64 <= full_hi;
     f16x8 ph[CT][2], pl[CT][BF16 ? 1 : 2];
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
       const float f = ks_now * qs[c];
+      uint32_t seen = 0;  // MASKED: of the lane's 16 tokens
+      if constexpr (MASKED) {
+        if (!full) seen = (uint32_t)(row_word(mask[c], s.n, actual(t)) >> (16 * g));
+      }
       float top = -INFINITY;  // of the 16 scores
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt)
@@ -213,7 +226,7 @@ __global__ __launch_bounds__(64 * KW, DIM == 256 ? 1 : 2) void k_kv_rows(KvAtten
           float y = x[c][tt][r] * f;
           if (!full) {
             const int j = t + 16 * g + 4 * tt + r;
-            y = j >= see[c].lo && j < see[c].hi ? y : -INFINITY;
+            y = (MASKED ? (seen >> (4 * tt + r) & 1) != 0 : j >= see[c].lo && j < see[c].hi) ? y : -INFINITY;
           }
           x[c][tt][r] = y;
           top = fmaxf(top, y);
@@ -365,7 +378,9 @@ __global__ __launch_bounds__(JT) void k_kv_join(KvAttention A, Partials P, uint3
   if (i >= s.n) return;
   const int group = A.a.q_heads / A.cache.kv_heads;
   const int r = i * group + h % group;
-  const Span span = row_span(A, s, r / (int)tile_rows * (int)tile_rows, (int)tile_rows, group);
+  const int first_row = r / (int)tile_rows * (int)tile_rows;
+  const Span span = A.masked ? row_span<true>(A, s, first_row, (int)tile_rows, group)
+                             : row_span<false>(A, s, first_row, (int)tile_rows, group);
   const int ns = (int)((span.end - span.begin + P.chunk - 1) / P.chunk);
   if (ns <= 1) return;
   const int64_t token = s.row + i, at = (token * A.a.q_heads + h) * P.nsplit;
@@ -412,25 +427,27 @@ __global__ __launch_bounds__(JT) void k_kv_join(KvAttention A, Partials P, uint3
     A.lse[token * A.a.q_heads + h] = (sum == 0.0f ? -INFINITY : mm + __log2f(sum)) * 0.69314718055994530942f;
 }
 
-template <int DIM, bool BF16>
+template <int DIM, bool BF16, bool MASKED>
 hipError_t launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
   const int64_t rows = a.batch.max_new * (a.a.q_heads / a.cache.kv_heads);
   const uint32_t tiles = (uint32_t)((rows + tile_rows - 1) / tile_rows);
   const uint32_t grid = (uint32_t)(a.batch.batch * a.cache.kv_heads * tiles * p.nsplit);
   if constexpr (DIM == 64 || (DIM == 128 && BF16)) {
     if (tile_rows == 32)
-      k_kv_rows<DIM, BF16, 2><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
+      k_kv_rows<DIM, BF16, 2, MASKED><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
     else
-      k_kv_rows<DIM, BF16, 1><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
+      k_kv_rows<DIM, BF16, 1, MASKED><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
   } else {
-    k_kv_rows<DIM, BF16, 1><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
+    k_kv_rows<DIM, BF16, 1, MASKED><<<grid, 64 * KW, 0, stream>>>(a, p, tiles);
   }
   return hipGetLastError();
 }
 
 template <int DIM>
 hipError_t launch(const KvAttention& a, const Partials& p, int tile_rows, hipStream_t stream) {
-  return a.bf16 ? launch<DIM, true>(a, p, tile_rows, stream) : launch<DIM, false>(a, p, tile_rows, stream);
+  if (a.masked)
+    return a.bf16 ? launch<DIM, true, true>(a, p, tile_rows, stream) : launch<DIM, false, true>(a, p, tile_rows, stream);
+  return a.bf16 ? launch<DIM, true, false>(a, p, tile_rows, stream) : launch<DIM, false, false>(a, p, tile_rows, stream);
 }
 
 }  // namespace
@@ -458,7 +475,9 @@ __global__ __launch_bounds__(JT) void k_kv_join_few(KvAttention A, Partials P, u
   if (i >= s.n) return;
   const int group = A.a.q_heads / A.cache.kv_heads;
   const int r = i * group + h % group;
-  const Span span = row_span(A, s, r / (int)tile_rows * (int)tile_rows, (int)tile_rows, group);
+  const int first_row = r / (int)tile_rows * (int)tile_rows;
+  const Span span = A.masked ? row_span<true>(A, s, first_row, (int)tile_rows, group)
+                             : row_span<false>(A, s, first_row, (int)tile_rows, group);
   const int ns = (int)((span.end - span.begin + P.chunk - 1) / P.chunk);
   if (ns <= 1) return;
   const int64_t token = s.row + i, at = (token * A.a.q_heads + h) * P.nsplit;

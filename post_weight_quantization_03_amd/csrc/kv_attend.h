@@ -25,10 +25,39 @@ __device__ __forceinline__ float value_exponent(float scale) {
 // Tokens of the cache that rows [r0, r0 + rows) of a sequence see, the first
 // rounded down to a multiple of 64.  A row is a query token and head of one key
 // head's group: row r is token r / group, head r % group.
+// MASKED: the first tokens that stay visible, up to a multiple of 64 (head), and the window follow each other
+// without what lies between: the span counts from 0, and count v stands for token v + (v >= head ? gap : 0).
+// Blocks are looked up only for tokens below `sinks` and from `lo` on.
 struct Span {
   int64_t begin, end;
+  int head, gap, sinks, lo;
+  __device__ __forceinline__ int token(int v) const { return v + (v >= head ? gap : 0); }
+  __device__ __forceinline__ int looked_up(int v) const {
+    const int t = token(v);
+    return t < sinks ? t : max(t, lo);
+  }
 };
-__device__ __forceinline__ Span row_span(const KvAttention& A, const Seq& s, int r0, int rows, int group) {
+template <bool MASKED>
+__device__ __forceinline__ Span row_span(const KvAttention& A, const Seq& s, int r0, int rows, int group);
+template <>
+__device__ __forceinline__ Span row_span<true>(const KvAttention& A, const Seq& s, int r0, int rows, int group) {
+  const int i0 = r0 / group, last = (r0 + rows < s.n * group ? r0 + rows : s.n * group) - 1;
+  const bool tree = A.mask.tree != nullptr;
+  const int before = s.len - s.n, p0 = tree ? before : before + i0, p1 = before + last / group;
+  int end = !tree && A.a.causal && p1 + 1 < s.len ? p1 + 1 : s.len;
+  if (end < 0) end = 0;
+  const int64_t lo = A.a.window > 0 ? p0 - A.a.window + 1 : 0;
+  const int sinks = (int)(A.mask.sinks < end ? A.mask.sinks : end), head = (sinks + 63) & ~63;
+  Span v{0, end, 0, 0, sinks, (int)(lo > 0 ? lo : 0)};
+  if (v.lo > head) {
+    v.head = head;
+    v.gap = (v.lo & ~63) - head;
+    v.end = end - v.gap > head ? end - v.gap : head;
+  }
+  return v;
+}
+template <>
+__device__ __forceinline__ Span row_span<false>(const KvAttention& A, const Seq& s, int r0, int rows, int group) {
   const int i0 = r0 / group, last = (r0 + rows < s.n * group ? r0 + rows : s.n * group) - 1;
   const int64_t p0 = (int64_t)s.len - s.n + i0, p1 = (int64_t)s.len - s.n + last / group;
   Span v;
@@ -36,6 +65,7 @@ __device__ __forceinline__ Span row_span(const KvAttention& A, const Seq& s, int
   v.begin = A.a.window > 0 && p0 - A.a.window + 1 > 0 ? p0 - A.a.window + 1 : 0;
   v.begin &= ~(int64_t)63;
   if (v.end < v.begin) v.end = v.begin;
+  v.head = v.gap = v.sinks = v.lo = 0;
   return v;
 }
 
@@ -50,6 +80,55 @@ __device__ __forceinline__ Sees row_sees(const KvAttention& A, const Seq& s, int
   int64_t lo = A.a.window > 0 && p - A.a.window + 1 > 0 ? p - A.a.window + 1 : 0;
   if (hi < lo) hi = lo;
   return {(int)lo, (int)hi};
+}
+
+// MASKED: tokens from lo to hi - 1 and below sinks (and hi) are seen by the row, and of the new tokens, from
+// hi = before on, those of its mask.
+struct RowMask {
+  int lo, hi, sinks;
+  const uint64_t* words;  // null without a tree
+};
+__device__ __forceinline__ RowMask row_mask(const KvAttention& A, const Seq& s, int r, int group, int32_t* st) {
+  if (r >= s.n * group) return {0, 0, 0, nullptr};
+  const int i = r / group, before = s.len - s.n;
+  const bool tree = A.mask.tree != nullptr;
+  int p = before + i;
+  if (tree && A.a.window > 0) {
+    p = A.mask.positions[s.row + i];
+    if (p < before || p >= s.len) {
+      raise_einval(st);
+      p = before;
+    }
+  }
+  const int hi = tree ? before : A.a.causal && p + 1 < s.len ? p + 1 : s.len;
+  const int64_t lo = A.a.window > 0 ? p - A.a.window + 1 : 0;
+  return {(int)(lo > 0 ? lo : 0), hi, (int)A.mask.sinks, tree ? A.mask.tree + (s.row + i) * A.mask.tree_stride : nullptr};
+}
+// The lowest n bits, for any n.
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1; }
+// Bit j: the row sees token t + j.
+__device__ __forceinline__ uint64_t row_word(const RowMask& m, int n, int t) {
+  uint64_t v = low_bits(m.hi - t) & (~low_bits(m.lo - t) | low_bits(m.sinks - t));
+  const int d = t - m.hi;
+  if (m.words && d > -64 && d < n) {
+    const int w = d >> 6, sh = d & 63;
+    uint64_t x = w >= 0 ? m.words[w] >> sh : 0;
+    if (sh > 0 && 64 * (w + 1) < n) x |= m.words[w + 1] << (64 - sh);
+    v |= x & low_bits(n - d);
+  }
+  return v;
+}
+// Tokens that every row of [r0, last] sees: from lo to hi - 1 and below sinks (and hi).
+struct Full {
+  int lo, hi, sinks;
+  __device__ __forceinline__ bool has(int t) const { return (t >= lo || t + 64 <= sinks) && t + 64 <= hi; }
+};
+__device__ __forceinline__ Full full_span(const KvAttention& A, const Seq& s, int r0, int last, int group) {
+  const int before = s.len - s.n;
+  const bool tree = A.mask.tree != nullptr;
+  const int p0 = before + r0 / group, p1 = tree ? s.len - 1 : before + last / group;
+  const int64_t lo = A.a.window > 0 ? p1 - A.a.window + 1 : 0;
+  return {(int)(lo > 0 ? lo : 0), tree ? before : A.a.causal && p0 + 1 < s.len ? p0 + 1 : s.len, (int)A.mask.sinks};
 }
 
 // 8 codes (two dwords) as fp16, exact: code + 128 = u becomes the low byte of the

@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 
 import post_weight_quantization_03_amd as _g
-from .attn import _empty, _elsewhere, _given, _one_device, _raw_stream
+from .attn import _apart, _empty, _elsewhere, _given, _one_device, _raw_stream
 
 _vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
 
@@ -98,7 +98,7 @@ def gptq_quantize_tokens(X, out: Tokens = None, stream=None) -> Tokens:
         out = Tokens(_empty((tokens, gptq_token_stride(cols)), X, stream, torch.int8),
                      _empty((tokens,), X, stream, torch.float32), _empty((tokens,), X, stream, torch.int32), cols)
     elif out.device != device:
-        raise ValueError(f"the Tokens are on device {out.device}, the call on {device}: a call's tensors are on one device")
+        raise _apart(device, out)
     elif out.tokens != tokens or out.cols != cols:
         raise ValueError("out must have X's tokens and cols")
     st = _g.lib().gptq_quantize_tokens(X.data_ptr(), _g._dtype_code(X), ldx, out.c, raw)
@@ -124,12 +124,12 @@ def gptq_int8_gemm(packed, scales, zeros, x: Tokens, Y=None, dtype=None, workspa
         if t.get_device() != device:
             raise _elsewhere(name, t, device)
     if x.device != device:
-        raise ValueError(f"the Tokens are on device {x.device}, the call on {device}: a call's tensors are on one device")
+        raise _apart(device, x)
     _refuse_gradients(torch, scales)
     rows = packed.shape[0]
-    if (packed.dim() != 2 or packed.element_size() != 4 or packed.shape[1] * 4 != x.cols or scales.dtype != torch.float32
-            or zeros.dtype != torch.uint8 or scales.numel() != rows or zeros.numel() != rows
-            or scales.shape[0] != rows or zeros.shape[0] != rows):
+    if (packed.dim() != 2 or packed.element_size() != 4 or packed.shape[1] * 4 != x.cols
+            or scales.dtype != torch.float32 or zeros.dtype != torch.uint8 or scales.numel() != rows
+            or zeros.numel() != rows or scales.shape[0] != rows or zeros.shape[0] != rows):
         raise ValueError("shape or dtype mismatch")
     if not packed.is_contiguous() or not scales.is_contiguous() or not zeros.is_contiguous():
         raise ValueError("packed, scales and zeros must be contiguous")

@@ -46,9 +46,9 @@ def check_tokens(q, x, poison=None):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-@pytest.mark.parametrize("tokens,cols", [(1, 1), (3, 7), (5, 8), (2, 127), (7, 128), (4, 129), (9, 511), (9, 513), (6, 2048),
-                                         (3, 2052), (5, 4096), (2, 4100), (3, 8192), (2, 11008), (1, 16384), (2, 16390),
-                                         (1, 40000), (1, 65536), (300, 640)])
+@pytest.mark.parametrize("tokens,cols", [(1, 1), (3, 7), (5, 8), (2, 127), (7, 128), (4, 129), (9, 511), (9, 513),
+                                         (6, 2048), (3, 2052), (5, 4096), (2, 4100), (3, 8192), (2, 11008), (1, 16384),
+                                         (2, 16390), (1, 40000), (1, 65536), (300, 640)])
 def test_quantize(tokens, cols, bf16):
     import post_weight_quantization_03_amd as g
     say(f"quantize {tokens} x {cols} bf16={bf16}")

@@ -77,8 +77,8 @@ def test_quantize_refusals():
 
 
 def gemm(t=None, packed=A, scales=A, zeros=A, rows=64, Y=A, dtype=0, ldy=64, ws=A, ws_bytes=1 << 40):
-    return g.lib().gptq_int8_gemm(packed, scales, zeros, rows, tokens() if t is None else t, Y, dtype, ldy, ws, ws_bytes,
-                                  None)
+    return g.lib().gptq_int8_gemm(packed, scales, zeros, rows, tokens() if t is None else t, Y, dtype, ldy, ws,
+                                  ws_bytes, None)
 
 
 def test_gemm_refusals():

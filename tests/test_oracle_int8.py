@@ -17,7 +17,8 @@ def nearest_even(q):
 def halves(rng, n):
     """A token with elements on and next to halves of its scale (1: the largest element is 127)."""
     k = rng.integers(-126, 126, n) + 0.5
-    x = np.where(rng.random(n) < 0.5, k, np.nextafter(k.astype(np.float32), np.float32(1000) * rng.choice([-1, 1], n).astype(np.float32)))
+    beside = np.nextafter(k.astype(np.float32), rng.choice([-1000, 1000], n).astype(np.float32))
+    x = np.where(rng.random(n) < 0.5, k, beside)
     x[0] = 127.0
     return x.astype(np.float32)
 
@@ -25,8 +26,8 @@ def halves(rng, n):
 @pytest.mark.parametrize("seed", range(4))
 def test_codes_against_exact_rationals(seed):
     rng = np.random.default_rng(seed)
-    x = np.stack([rng.standard_normal(40).astype(np.float32) * np.float32(10.0 ** rng.integers(-30, 30)), halves(rng, 40),
-                  np.zeros(40, np.float32)])
+    far = rng.standard_normal(40).astype(np.float32) * np.float32(10.0 ** rng.integers(-30, 30))
+    x = np.stack([far, halves(rng, 40), np.zeros(40, np.float32)])
     codes, scales, sums = R.quantize_tokens(x)
     for t in range(3):
         s = Fraction(float(scales[t]))
