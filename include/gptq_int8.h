@@ -33,7 +33,7 @@ typedef struct {
   int32_t* sums;  /* [tokens]: of a token's codes */
   int64_t tokens;
   int64_t cols;   /* 1 <= cols <= 65536 */
-  int64_t stride; /* >= gptq_token_stride(cols), a multiple of 16 */
+  int64_t stride; /* >= gptq_token_stride(cols), a multiple of 16, at most 2^22 */
 } gptq_tokens;
 
 /* cols rounded up to a multiple of 128; 0 when cols is out of range. */
@@ -59,14 +59,9 @@ int gptq_quantize_tokens(const void* X, gptq_dtype x_dtype, int64_t ldx, const g
  * rounded to fp32, multiplied by the token's scale, then the row's, and rounded to
  * y_dtype: the order of the sum does not matter, so results do not depend on how a
  * call is split, and are bit-reproducible.
- * workspace: gptq_int8_gemm_workspace_bytes(rows, cols, tokens) bytes, 16-byte aligned
- * (NULL when that is 0).  Y must not overlap the inputs or the workspace.
- * tokens == 0 or rows == 0: no work. */
-size_t gptq_int8_gemm_workspace_bytes(int64_t rows, int64_t cols, int64_t tokens);
-
+ * No workspace.  Y must not overlap the inputs.  tokens == 0 or rows == 0: no work. */
 int gptq_int8_gemm(const uint32_t* packed, const float* scales, const uint8_t* zeros, int64_t rows,
-                   const gptq_tokens* x, void* Y, gptq_dtype y_dtype, int64_t ldy, void* workspace,
-                   size_t workspace_bytes, gptq_stream_t stream);
+                   const gptq_tokens* x, void* Y, gptq_dtype y_dtype, int64_t ldy, gptq_stream_t stream);
 
 #ifdef __cplusplus
 }

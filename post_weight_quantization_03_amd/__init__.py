@@ -404,5 +404,4 @@ from .attn import (KVBatch, KVCache, KVTree, Rope, gptq_kv_append, gptq_kv_atten
                    gptq_kv_attention_workspace_bytes, gptq_kv_read, gptq_kv_tree, gptq_qk_norm_rope,
                    gptq_qk_norm_rope_backward, gptq_qk_norm_rope_backward_workspace_bytes)
 from . import int8  # noqa: E402
-from .int8 import (Tokens, gptq_int8_gemm, gptq_int8_gemm_workspace_bytes, gptq_quantize_tokens,  # noqa: E402,F401
-                   gptq_token_stride)
+from .int8 import Tokens, gptq_int8_gemm, gptq_quantize_tokens, gptq_token_stride  # noqa: E402,F401

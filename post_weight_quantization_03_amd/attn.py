@@ -600,7 +600,8 @@ def gptq_kv_tree(batch: KVBatch, parents, window: int = 0, sinks: int = 0, out: 
             raise _apart(device, out)
         _check_tree(out, batch)
     st = _g.lib().gptq_kv_tree(batch.c, parents.data_ptr(), window, sinks, out.positions.data_ptr(),
-                               out.mask.data_ptr(), out.stride, None if d_status is None else _status(d_status, device), raw)
+                               out.mask.data_ptr(), out.stride,
+                               None if d_status is None else _status(d_status, device), raw)
     if st:
         raise _g.GptqError(st, "gptq_kv_tree")
     out.window, out.sinks = window, sinks

@@ -7,6 +7,7 @@
 namespace gptq {
 
 constexpr int64_t INT8_MAX_COLS = 65536;  // 255 * 127 * 65536 < 2^31
+constexpr int64_t INT8_MAX_STRIDE = (int64_t)1 << 22;  // 256 tokens lie within 2^30 bytes
 constexpr int64_t INT8_PAD = 128;         // codes of a token are padded with zeros to a multiple of this
 
 struct QuantTokens {
@@ -28,11 +29,14 @@ struct Int8Gemm {
   void* Y;
   int64_t ldy;
   int bf16;
-  int32_t* workspace;
 };
-size_t int8_gemm_workspace(int64_t rows, int64_t cols, int64_t tokens);
+// Whether the launch stays below 2^32 threads.
 bool int8_gemm_fits(int64_t rows, int64_t cols, int64_t tokens);
 hipError_t int8_gemm(const Int8Gemm& a, hipStream_t stream);
+// k_int8_rows.hip: up to 16 tokens.  k_int8_tile.hip: tiles of rows x tokens.
+hipError_t int8_rows_launch(const Int8Gemm& a, hipStream_t stream);
+enum class Int8Form { T256x256, T256x128, T128x64, T64x64, T32x32, T32x16 };
+hipError_t int8_tile_launch(const Int8Gemm& a, Int8Form form, hipStream_t stream);
 
 #ifdef __HIPCC__
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
@@ -48,9 +52,11 @@ constexpr uint32_t NOWHERE = 0x7ffffff0u;  // an offset past every buffer here
 // Codes of a layer, 0 to 255, as int8: code - 128.
 __device__ __forceinline__ i32x4 signed_codes(i32x4 w) { return w ^ (int32_t)0x80808080; }
 
-// Sum of (code - 128) * x to a value: the rest of the zero point, then the scales.
-__device__ __forceinline__ float int8_value(int32_t sum, int32_t zero, int32_t token_sum, float token_scale, float scale) {
-  return (float)(sum + (128 - zero) * token_sum) * token_scale * scale;
+// Sum of (code - 128) * x to a value: what the zero point adds (rest = 128 - zero point, and a token's sum is
+// below 2^23), then the scales.
+__device__ __forceinline__ float int8_value(int32_t sum, int32_t rest, int32_t token_sum, float token_scale,
+                                            float scale) {
+  return (float)(sum + __mul24(rest, token_sum)) * token_scale * scale;
 }
 __device__ __forceinline__ void int8_store(void* Y, int64_t at, float y, bool bf16) {
   if (bf16)

@@ -15,7 +15,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 int tokens_check(const gptq_tokens* x) {
   if (!x || x->tokens < 0 || x->tokens > MAX_DIM || x->cols < 1) return GPTQ_EINVAL;
   if (x->cols > INT8_MAX_COLS) return GPTQ_EUNSUPPORTED;
-  if (x->stride < gptq_token_stride(x->cols) || x->stride % 16 != 0 || x->stride > MAX_DIM) return GPTQ_EINVAL;
+  if (x->stride < gptq_token_stride(x->cols) || x->stride % 16 != 0) return GPTQ_EINVAL;
+  if (x->stride > INT8_MAX_STRIDE) return GPTQ_EUNSUPPORTED;
   return GPTQ_OK;
 }
 bool tokens_pointers(const gptq_tokens* x) {
@@ -48,14 +49,8 @@ int gptq_quantize_tokens(const void* X, gptq_dtype x_dtype, int64_t ldx, const g
   return quantize_tokens(a, (hipStream_t)stream) == hipSuccess ? GPTQ_OK : GPTQ_EHIP;
 }
 
-size_t gptq_int8_gemm_workspace_bytes(int64_t rows, int64_t cols, int64_t tokens) {
-  if (rows <= 0 || rows > MAX_DIM || cols < 1 || cols > INT8_MAX_COLS || tokens <= 0 || tokens > MAX_DIM) return 0;
-  return int8_gemm_workspace(rows, cols, tokens);
-}
-
 int gptq_int8_gemm(const uint32_t* packed, const float* scales, const uint8_t* zeros, int64_t rows,
-                   const gptq_tokens* x, void* Y, gptq_dtype y_dtype, int64_t ldy, void* workspace,
-                   size_t workspace_bytes, gptq_stream_t stream) {
+                   const gptq_tokens* x, void* Y, gptq_dtype y_dtype, int64_t ldy, gptq_stream_t stream) {
   const int st = tokens_check(x);
   if (st != GPTQ_OK) return st;
   if (rows < 0 || rows > MAX_DIM || !dtype_ok(y_dtype) || x->cols % 4 != 0 || ldy < rows || ldy > ((int64_t)1 << 40))
@@ -65,10 +60,7 @@ int gptq_int8_gemm(const uint32_t* packed, const float* scales, const uint8_t* z
       !aligned(Y, (uintptr_t)elem_size(y_dtype)) || !tokens_pointers(x))
     return GPTQ_EINVAL;
   if (!int8_gemm_fits(rows, x->cols, x->tokens)) return GPTQ_EUNSUPPORTED;
-  const size_t need = int8_gemm_workspace(rows, x->cols, x->tokens);
-  if (workspace_bytes < need || (need > 0 && !workspace)) return GPTQ_EWORKSPACE;
-  if (need > 0 && !aligned(workspace, 16)) return GPTQ_EINVAL;
-  Int8Gemm a{packed, scales, zeros, rows, *x, Y, ldy, y_dtype == GPTQ_BF16, static_cast<int32_t*>(workspace)};
+  const Int8Gemm a{packed, scales, zeros, rows, *x, Y, ldy, y_dtype == GPTQ_BF16};
   return int8_gemm(a, (hipStream_t)stream) == hipSuccess ? GPTQ_OK : GPTQ_EHIP;
 }
 

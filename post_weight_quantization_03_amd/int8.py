@@ -12,9 +12,9 @@ from __future__ import annotations
 import ctypes
 
 import post_weight_quantization_03_amd as _g
-from .attn import _apart, _empty, _elsewhere, _given, _one_device, _raw_stream
+from .attn import _apart, _elsewhere, _empty, _one_device, _raw_stream
 
-_vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+_vp, _i64 = ctypes.c_void_p, ctypes.c_int64
 
 
 class gptq_tokens(ctypes.Structure):
@@ -28,9 +28,7 @@ def bind(L):
     L.gptq_token_stride.restype = _i64
     L.gptq_quantize_tokens.argtypes = [_vp, ci, _i64, P(gptq_tokens), _vp]
     L.gptq_quantize_tokens.restype = ci
-    L.gptq_int8_gemm_workspace_bytes.argtypes = [_i64, _i64, _i64]
-    L.gptq_int8_gemm_workspace_bytes.restype = _sz
-    L.gptq_int8_gemm.argtypes = [_vp, _vp, _vp, _i64, P(gptq_tokens), _vp, ci, _i64, _vp, _sz, _vp]
+    L.gptq_int8_gemm.argtypes = [_vp, _vp, _vp, _i64, P(gptq_tokens), _vp, ci, _i64, _vp]
     L.gptq_int8_gemm.restype = ci
 
 
@@ -107,11 +105,7 @@ def gptq_quantize_tokens(X, out: Tokens = None, stream=None) -> Tokens:
     return out
 
 
-def gptq_int8_gemm_workspace_bytes(rows: int, cols: int, tokens: int) -> int:
-    return int(_g.lib().gptq_int8_gemm_workspace_bytes(rows, cols, tokens))
-
-
-def gptq_int8_gemm(packed, scales, zeros, x: Tokens, Y=None, dtype=None, workspace=None, stream=None):
+def gptq_int8_gemm(packed, scales, zeros, x: Tokens, Y=None, dtype=None, stream=None):
     """Y [tokens, rows] (bf16 unless `dtype` or Y says fp32) = the tokens through the layer of packed
     [rows, cols / 4] 8-bit codes (int32 words), scales fp32 and zeros uint8 [rows] or [rows, 1]."""
     torch = _g._torch()
@@ -119,7 +113,7 @@ def gptq_int8_gemm(packed, scales, zeros, x: Tokens, Y=None, dtype=None, workspa
     raw = _raw_stream(torch, device, stream)
     if raw is None:
         with torch.cuda.device(device):
-            return gptq_int8_gemm(packed, scales, zeros, x, Y, dtype, workspace, stream)
+            return gptq_int8_gemm(packed, scales, zeros, x, Y, dtype, stream)
     for name, t in (("scales", scales), ("zeros", zeros)):
         if t.get_device() != device:
             raise _elsewhere(name, t, device)
@@ -140,14 +134,8 @@ def gptq_int8_gemm(packed, scales, zeros, x: Tokens, Y=None, dtype=None, workspa
         ldy = _matrix("Y", Y, device)
         if tuple(Y.shape) != (x.tokens, rows) or dtype is not None and Y.dtype != dtype:
             raise ValueError("shape or dtype mismatch")
-    L = _g.lib()
-    if workspace is None:
-        need = L.gptq_int8_gemm_workspace_bytes(rows, x.cols, x.tokens)
-        if need:
-            workspace = _g._workspace(need, scales, stream)
-    wp, wn = (None, 0) if workspace is None else _given("workspace", workspace, device)
-    st = L.gptq_int8_gemm(packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), rows, x.c, Y.data_ptr(),
-                          _g._dtype_code(Y), ldy, wp, wn, raw)
+    st = _g.lib().gptq_int8_gemm(packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), rows, x.c, Y.data_ptr(),
+                                 _g._dtype_code(Y), ldy, raw)
     if st:
         raise _g.GptqError(st, "gptq_int8_gemm")
     return Y

@@ -20,7 +20,7 @@ E, U, OK = g.GPTQ_EINVAL, g.GPTQ_EUNSUPPORTED, g.GPTQ_OK
 def test_every_declared_symbol_is_exported():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"\b(gptq_[a-z0-9_]+)\s*\(", text))
-    assert names == {"gptq_token_stride", "gptq_quantize_tokens", "gptq_int8_gemm", "gptq_int8_gemm_workspace_bytes"}
+    assert names == {"gptq_token_stride", "gptq_quantize_tokens", "gptq_int8_gemm"}
     for lib in (g.lib(), ctypes.CDLL(os.path.join(os.path.dirname(g.LIB_PATH), "libgptq_trace.so"))):
         for n in names:
             assert hasattr(lib, n), n
@@ -31,7 +31,7 @@ def test_every_declared_symbol_is_exported():
 def test_header_is_plain_c(tmp_path):
     src = tmp_path / "user.c"
     src.write_text('#include "gptq_int8.h"\nint main(void) { gptq_tokens t = {0};\n'
-                   '  return gptq_int8_gemm(0, 0, 0, 0, &t, 0, GPTQ_BF16, 0, 0, 0, 0); }\n')
+                   '  return gptq_int8_gemm(0, 0, 0, 0, &t, 0, GPTQ_BF16, 0, 0); }\n')
     r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-fsyntax-only", "-I",
                         os.path.dirname(HEADER), str(src)], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
@@ -65,6 +65,8 @@ def test_quantize_refusals():
     assert quantize(tokens(cols=65537, stride=66000), ldx=65537) == U
     assert quantize(tokens(stride=128)) == E
     assert quantize(tokens(stride=264)) == E
+    assert quantize(tokens(stride=(1 << 22) + 16)) == U
+    assert quantize(tokens(stride=1 << 62)) == U
     assert quantize(tokens(), dtype=2) == E
     assert quantize(tokens(), ldx=255) == E
     assert quantize(tokens(), X=None) == E
@@ -76,9 +78,8 @@ def test_quantize_refusals():
     assert quantize(tokens(n=1 << 22, cols=8193, stride=8320), ldx=8193) == U  # 1024 threads each
 
 
-def gemm(t=None, packed=A, scales=A, zeros=A, rows=64, Y=A, dtype=0, ldy=64, ws=A, ws_bytes=1 << 40):
-    return g.lib().gptq_int8_gemm(packed, scales, zeros, rows, tokens() if t is None else t, Y, dtype, ldy, ws,
-                                  ws_bytes, None)
+def gemm(t=None, packed=A, scales=A, zeros=A, rows=64, Y=A, dtype=0, ldy=64):
+    return g.lib().gptq_int8_gemm(packed, scales, zeros, rows, tokens() if t is None else t, Y, dtype, ldy, None)
 
 
 def test_gemm_refusals():
@@ -98,24 +99,6 @@ def test_gemm_refusals():
     assert gemm(t=tokens(n=1 << 30), rows=1 << 30, ldy=1 << 30) == U
 
 
-def test_workspace_bytes_of_sizes_out_of_range():
-    f = g.lib().gptq_int8_gemm_workspace_bytes
-    for rows, cols, n in ((0, 128, 1), (-1, 128, 1), (16, 0, 1), (16, 65540, 1), (16, 128, 0), (1 << 31, 128, 1),
-                          (16, 128, 1 << 31)):
-        assert f(rows, cols, n) == 0
-
-
-def test_short_workspace_is_refused():
-    f = g.lib().gptq_int8_gemm_workspace_bytes
-    cases = [(r, c, n) for r in (64, 1000, 4096) for c in (256, 4096, 65536) for n in (1, 40, 200, 1000) if f(r, c, n)]
-    for rows, cols, n in cases:
-        t = tokens(n=n, cols=cols, stride=cols)
-        need = f(rows, cols, n)
-        assert gemm(t=t, rows=rows, ldy=rows, ws_bytes=need - 1) == g.GPTQ_EWORKSPACE
-        assert gemm(t=t, rows=rows, ldy=rows, ws=None, ws_bytes=need) == g.GPTQ_EWORKSPACE
-        assert gemm(t=t, rows=rows, ldy=rows, ws=A + 4, ws_bytes=need) == E
-
-
 def test_binding_refusals():
     import torch
     with pytest.raises(ValueError):
@@ -133,7 +116,7 @@ def arguments(odd=None):
             "scales": t("scales", (3,), torch.float32), "sums": t("sums", (3,), torch.int32),
             "packed": WordTensor((16, 64), torch.int32, 0 if odd == "packed" else 1),
             "w_scales": t("w_scales", (16, 1), torch.float32), "zeros": t("zeros", (16, 1), torch.uint8),
-            "Y": t("Y", (3, 16), torch.bfloat16), "workspace": t("workspace", (64,), torch.uint8)}
+            "Y": t("Y", (3, 16), torch.bfloat16)}
 
 
 class WordTensor(Tensor):
@@ -146,8 +129,8 @@ def made(a):
 
 
 CALLS = {"gptq_quantize_tokens": (("X", "codes", "scales", "sums"), lambda a: g.gptq_quantize_tokens(a["X"], made(a))),
-         "gptq_int8_gemm": (("packed", "w_scales", "zeros", "codes", "Y", "workspace"), lambda a: g.gptq_int8_gemm(
-             a["packed"], a["w_scales"], a["zeros"], made(a), a["Y"], workspace=a["workspace"]))}
+         "gptq_int8_gemm": (("packed", "w_scales", "zeros", "codes", "Y"), lambda a: g.gptq_int8_gemm(
+             a["packed"], a["w_scales"], a["zeros"], made(a), a["Y"]))}
 
 
 @pytest.mark.parametrize("name", CALLS)
