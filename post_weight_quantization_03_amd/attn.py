@@ -277,9 +277,23 @@ class KVTree:
         _int32("positions", positions, self.device, (mask.shape[0],))
         if mask.dim() != 2 or mask.dtype != torch.int64 or mask.stride(1) != 1 and mask.shape[1] > 1:
             raise ValueError("mask must be an int64 [total, words] device tensor with unit stride in a row")
+        total, words = mask.shape
+        self._hold(positions, mask, total, words, mask.stride(0) if total > 1 else words, window, sinks)
+
+    def _hold(self, positions, mask, total, words, stride, window, sinks):
         self.positions, self.mask, self.window, self.sinks = positions, mask, window, sinks
-        self.total, self.words = mask.shape
-        self.stride = mask.stride(0) if self.total > 1 else self.words
+        self.total, self.words, self.stride = total, words, stride
+
+    @classmethod
+    def _new(cls, batch, stream):
+        """Room made for a call on `stream`."""
+        torch = _g._torch()
+        t = cls.__new__(cls)
+        t.device = batch.device
+        total, words = batch.total, -(-batch.max_new // 64)
+        t._hold(_empty((total,), batch.kv_len, stream, torch.int32),
+                _empty((total, words), batch.kv_len, stream, torch.int64), total, words, words, None, None)
+        return t
 
     @classmethod
     def empty(cls, batch: KVBatch):
@@ -593,8 +607,7 @@ def gptq_kv_tree(batch: KVBatch, parents, window: int = 0, sinks: int = 0, out: 
             return gptq_kv_tree(batch, parents, window, sinks, out, d_status, stream)
     _int32("parents", parents, device, (batch.total,))
     if out is None:
-        out = KVTree(_empty((batch.total,), batch.kv_len, stream, torch.int32),
-                     _empty((batch.total, -(-batch.max_new // 64)), batch.kv_len, stream, torch.int64))
+        out = KVTree._new(batch, stream)
     else:
         if out.device != device:
             raise _apart(device, out)

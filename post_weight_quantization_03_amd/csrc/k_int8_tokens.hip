@@ -4,9 +4,12 @@
 // a wave (up to 512 elements), 256 or 1024 threads, so X is read once.  The largest element is
 // taken over the bits without the sign, as integers: infinity and NaN come out above every number.
 //
-// The code is the nearest integer to x / s, exactly: x * (1 / s) rounds to it or to its
-// neighbour across a half, and the rest e = x - q s (one fma, exact where |e| is near s / 2:
-// a multiple of the smaller of x's and s's last places, and at most s) decides.
+// The code is the nearest integer to x / s, exactly.  x * (1 / s) + 1.5 * 2^23 rounds to a number whose last
+// byte is it or its neighbour across a half, and the rest e = x - q s (one fma, exact where |e| is near s / 2:
+// a multiple of the smaller of x's and s's last places, and at most s) tells: below s / 2 it is the nearest.  The
+// largest |e| of a thread's eight elements is looked at, so only those with one on a half or across it are
+// done over: 4 VALU instructions an element beside the packing, which with 11 (every element decided for itself)
+// took 19 us for 4096 x 4096 in bf16.
 #include "int8.h"
 
 namespace gptq {
@@ -22,12 +25,35 @@ __device__ __forceinline__ uint32_t element(const void* p, int64_t i) {
     return static_cast<const uint32_t*>(p)[i];
 }
 
-__device__ __forceinline__ int32_t code_of(float x, float scale, float inv) {
-  float q = __builtin_rintf(x * inv);
-  const float e = fmaf(-q, scale, x), twice = 2.0f * fabsf(e);
-  const bool odd = ((int32_t)q & 1) != 0;
-  if (twice > scale || (twice == scale && odd)) q += __builtin_copysignf(1.0f, e);
-  return (int32_t)q;
+constexpr float MAGIC = 12582912.0f;  // 1.5 * 2^23
+
+// Four codes out of the last bytes.
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x00000400u), __builtin_amdgcn_perm(b, a, 0x00000400u),
+                               0x05040100u);
+}
+
+// Eight codes of x / scale, inv near 1 / scale.
+__device__ __forceinline__ uint2 codes_of(const uint32_t (&x)[8], float scale, float inv) {
+  float q[8], most = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float v = __uint_as_float(x[j]);
+    q[j] = fmaf(v, inv, MAGIC);
+    most = fmaxf(most, fabsf(fmaf(-(q[j] - MAGIC), scale, v)));
+  }
+  if (2.0f * most >= scale) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float e = fmaf(-(q[j] - MAGIC), scale, __uint_as_float(x[j])), twice = 2.0f * fabsf(e);
+      const bool odd = (__float_as_uint(q[j]) & 1) != 0;
+      if (twice > scale || (twice == scale && odd)) q[j] += __builtin_copysignf(1.0f, e);
+    }
+  }
+  uint32_t u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(q[j]);
+  return make_uint2(pack4(u[0], u[1], u[2], u[3]), pack4(u[4], u[5], u[6], u[7]));
 }
 
 // NT threads a token, 8 NI elements a thread.
@@ -83,18 +109,10 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_quantize_tokens(QuantTo
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int k = 8 * (tid + NT * i);
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      w[h] = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int32_t q = finite ? code_of(__uint_as_float(x[i][4 * h + j]), scale, inv) : 0;
-        w[h] |= (uint32_t)(q & 0xff) << (8 * j);
-      }
-      sum = __builtin_amdgcn_sdot4((int)w[h], 0x01010101, sum, false);
-    }
-    if (k < stride) *reinterpret_cast<uint2*>(out + k) = make_uint2(w[0], w[1]);
+    const uint2 w = finite ? codes_of(x[i], scale, inv) : make_uint2(0, 0);
+    sum = __builtin_amdgcn_sdot4((int)w.x, 0x01010101, sum, false);
+    sum = __builtin_amdgcn_sdot4((int)w.y, 0x01010101, sum, false);
+    if (k < stride) *reinterpret_cast<uint2*>(out + k) = w;
   }
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);

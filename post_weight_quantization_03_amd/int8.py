@@ -55,8 +55,27 @@ class Tokens:
         stride = codes.stride(0) if n > 1 else codes.shape[1]
         if stride < codes.shape[1] or stride % 16:
             raise ValueError("codes must have a row stride of whole 16 bytes")
+        self._hold(codes, scales, sums, n, cols, stride)
+
+    def _hold(self, codes, scales, sums, n, cols, stride):
         self.codes, self.scales, self.sums, self.tokens, self.cols = codes, scales, sums, n, cols
         self.c = gptq_tokens(codes.data_ptr(), scales.data_ptr(), sums.data_ptr(), n, cols, stride)
+
+    @classmethod
+    def _new(cls, like, stream, device, tokens, cols):
+        """Room made for a call on `stream`, on like's device."""
+        torch = _g._torch()
+        stride = gptq_token_stride(cols)
+        t = cls.__new__(cls)
+        t.device = device
+        if stream is None:
+            make = like.new_empty
+            t._hold(make((tokens, stride), dtype=torch.int8), make(tokens, dtype=torch.float32),
+                    make(tokens, dtype=torch.int32), tokens, cols, stride)
+        else:
+            t._hold(_empty((tokens, stride), like, stream, torch.int8), _empty((tokens,), like, stream, torch.float32),
+                    _empty((tokens,), like, stream, torch.int32), tokens, cols, stride)
+        return t
 
     @classmethod
     def empty(cls, tokens: int, cols: int, device):
@@ -93,8 +112,7 @@ def gptq_quantize_tokens(X, out: Tokens = None, stream=None) -> Tokens:
     ldx = _matrix("X", X, device)
     tokens, cols = X.shape
     if out is None:
-        out = Tokens(_empty((tokens, gptq_token_stride(cols)), X, stream, torch.int8),
-                     _empty((tokens,), X, stream, torch.float32), _empty((tokens,), X, stream, torch.int32), cols)
+        out = Tokens._new(X, stream, device, tokens, cols)
     elif out.device != device:
         raise _apart(device, out)
     elif out.tokens != tokens or out.cols != cols:
