@@ -12,8 +12,9 @@ namespace {
 
 constexpr int LOCAL = 8192;
 
-__global__ __launch_bounds__(256) void k_kv_tree(gptq_kv_batch B, const int32_t* parents, int64_t window, int64_t sinks,
-                                                 int32_t* positions, uint64_t* tree, int64_t stride, int32_t* d_status) {
+__global__ __launch_bounds__(256) void k_kv_tree(gptq_kv_batch B, const int32_t* parents, int64_t window,
+                                                 int64_t sinks, int32_t* positions, uint64_t* tree, int64_t stride,
+                                                 int32_t* d_status) {
   __shared__ int32_t local[LOCAL];
   const Seq s = load_seq(B, (int)blockIdx.x, d_status);
   const int n = s.n, before = s.len - n, words = (int)((B.max_new + 63) / 64);

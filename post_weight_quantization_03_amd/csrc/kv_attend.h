@@ -102,10 +102,13 @@ __device__ __forceinline__ RowMask row_mask(const KvAttention& A, const Seq& s, 
   }
   const int hi = tree ? before : A.a.causal && p + 1 < s.len ? p + 1 : s.len;
   const int64_t lo = A.a.window > 0 ? p - A.a.window + 1 : 0;
-  return {(int)(lo > 0 ? lo : 0), hi, (int)A.mask.sinks, tree ? A.mask.tree + (s.row + i) * A.mask.tree_stride : nullptr};
+  return {(int)(lo > 0 ? lo : 0), hi, (int)A.mask.sinks,
+          tree ? A.mask.tree + (s.row + i) * A.mask.tree_stride : nullptr};
 }
 // The lowest n bits, for any n.
-__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1; }
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1;
+}
 // Bit j: the row sees token t + j.
 __device__ __forceinline__ uint64_t row_word(const RowMask& m, int n, int t) {
   uint64_t v = low_bits(m.hi - t) & (~low_bits(m.lo - t) | low_bits(m.sinks - t));

@@ -206,6 +206,27 @@ def test_trees_of_split_sequences(form, bf16, mask):
     check(c, new, qh, bf16, sees, *mask, tree=lambda plan: g.gptq_kv_tree(plan, to_dev(parents), *mask))
 
 
+@pytest.mark.parametrize("form", [
+    ([5000, 90, 2000, 64, 3000], [70, 70, 1, 64, 30], 4, 2, 128, 64), ([700, 6000, 300], [200, 150, 0], 6, 2, 64, 16),
+    ([40 + 37 * i for i in range(64)], [1 + i % 40 for i in range(64)], 4, 1, 64, 32),
+    ([1500, 400], [90, 90], 4, 4, 256, 128), ([3000, 1], [140, 1], 4, 2, 128, 16)])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("mask", [(0, 0), (900, 4)])
+def test_trees_of_unequal_sequences(form, bf16, mask):
+    """Batches of very different lengths over the prompt kernel's splits: run to run the same bits."""
+    import post_weight_quantization_03_amd as g
+    lengths, new, qh, kh, dim, block = form
+    say(f"unequal trees of {len(new)} sequences, dim {dim} bf16={bf16} mask={mask}")
+    torch, _ = torch_dev()
+    got = []
+    for _ in range(2):
+        rng = np.random.default_rng(58)
+        c = Paged(rng, lengths, kh, block, dim)
+        parents, sees = trees(rng, new, lengths, *mask)
+        got.append(check(c, new, qh, bf16, sees, *mask, tree=lambda plan: g.gptq_kv_tree(plan, to_dev(parents), *mask)))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 @pytest.mark.parametrize("new,qh", [(9, 2), (100, 2), (140, 4)])
 def test_any_pattern(new, qh):
     """Masks that are no trees: later tokens, not oneself, nothing at all; wider rows than needed and bits
@@ -228,6 +249,26 @@ def test_any_pattern(new, qh):
     sees = [M.tree_sees(np.zeros(new), a, t - new) for a, t in zip(among, length)]
     for bf16 in (True, False):
         check(c, [new, new], qh, bf16, sees, tree=lambda plan: tree)
+
+
+@pytest.mark.parametrize("new", [3, 80])
+def test_rows_that_no_sequence_has_stay(new):
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    rng = np.random.default_rng(60)
+    c = Paged(rng, [500, 3000], 2, 16, 128)
+    total = 2 * new + 5
+    lens = to_dev(np.array([500, 3000], np.int32))
+    plan = g.KVBatch(to_dev(np.array([2, 2 + new, 2 + 2 * new], np.int32)), lens, to_dev(c.table), total, new, 3000)
+    q = on_device(values(rng, (total, 4, 128), True), True)
+    tree = g.gptq_kv_tree(plan, torch.full((total,), -1, dtype=torch.int32, device=dev), 100, 4)
+    for kw in ({"window": 100, "sinks": 4}, {"tree": g.gptq_kv_tree(plan, torch.full_like(tree.positions, -1))},
+               {"window": 100, "sinks": 4, "tree": tree}):
+        out, lse = torch.full_like(q, 7.0), torch.full((total, 4), 7.0, device=dev)
+        g.gptq_kv_attention(q, c.dev, plan, out=out, lse=lse, **kw)
+        apart = [0, 1, *range(2 + 2 * new, total)]
+        assert (out[apart] == 7).all() and (lse[apart] == 7).all()
+        assert not (lse[2:2 + 2 * new] == 7).any()
 
 
 def test_a_chain_is_plain_attention():
@@ -318,6 +359,26 @@ def test_index_data_out_of_range():
     assert int(st) == g.GPTQ_EINVAL and torch.equal(t.mask[8:], tree.mask[8:])
 
 
+def test_lengths_out_of_range_among_unequal_trees():
+    """A sequence whose length is out of range raises the status, and others are not affected."""
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    rng = np.random.default_rng(59)
+    new, lengths = [70, 70, 70], [900, 4000, 300]
+    c = Paged(rng, lengths, 2, 16, 64)
+    plan, _ = c.plan(new)
+    parents, _ = trees(rng, new, lengths)
+    q = on_device(values(rng, (210, 4, 64), True), True)
+    tree = g.gptq_kv_tree(plan, to_dev(parents))
+    want = g.gptq_kv_attention(q, c.dev, plan, tree=tree)
+    for bad in (-1, 4001, 2 ** 31 - 1):
+        st = to_dev(np.zeros(1, np.int32))
+        wrong = g.KVBatch(plan.q_start, to_dev(np.array([900, 4000, bad], np.int32)), plan.block_table, 210, 70, 4000)
+        got = g.gptq_kv_attention(q, c.dev, wrong, tree=tree, d_status=st)
+        assert int(st) == g.GPTQ_EINVAL
+        assert torch.equal(got[:140], want[:140])
+
+
 @pytest.mark.parametrize("new", [6, 100])
 def test_nan_scales_of_blocks_that_are_not_seen(new):
     """Blocks between the first tokens and the window, and drafted tokens of other branches, may hold
@@ -357,8 +418,8 @@ def test_another_stream_and_replayed_graphs(new, length):
         parents = to_dev(np.concatenate([random_parents(rng, new)] * 2).astype(np.int32))
         q = on_device(values(rng, (2 * new, 4, 128), True), True)
         out, tree = torch.empty_like(q), g.KVTree.empty(plan)
-        space = torch.empty(max(1, g.gptq_kv_attention_workspace_bytes(c.dev, plan, 4, g.GPTQ_BF16, True, 2000, 4)),
-                            dtype=torch.uint8, device=dev)
+        need = g.gptq_kv_attention_workspace_bytes(c.dev, plan, 4, g.GPTQ_BF16, True, 2000, 4)
+        space = torch.full((need + 64,), 255, dtype=torch.uint8, device=dev)
 
         def step():
             g.gptq_kv_tree(plan, parents, 2000, 4, out=tree)
@@ -371,9 +432,9 @@ def test_another_stream_and_replayed_graphs(new, length):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             step()
-        graphs.append((graph, plan, lens, parents, q, out))
+        graphs.append((graph, plan, lens, parents, q, out, space))
     for turn in range(3):
-        for graph, plan, lens, parents, q, out in graphs:
+        for graph, plan, lens, parents, q, out, space in graphs:
             parents.copy_(to_dev(np.concatenate([random_parents(rng, new) for _ in range(2)]).astype(np.int32)))
             lens.copy_(to_dev(np.array([length + 50 - 7 * turn, length - 100 * turn], np.int32)))
             side.wait_stream(torch.cuda.current_stream())
@@ -382,3 +443,4 @@ def test_another_stream_and_replayed_graphs(new, length):
             eager = g.gptq_kv_attention(q, c.dev, plan, window=2000, sinks=4, tree=tree, stream=side)
             torch.cuda.synchronize()
             assert torch.equal(out, eager)
+            assert (space[space.numel() - 64:] == 255).all()
