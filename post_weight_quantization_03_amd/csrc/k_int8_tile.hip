@@ -26,6 +26,9 @@ namespace {
 typedef __attribute__((address_space(3))) char lds_char;
 typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
 typedef float f32x8i __attribute__((ext_vector_type(8)));
+// of any element alignment
+typedef float f32x4e __attribute__((ext_vector_type(4), aligned(4)));
+typedef __bf16 bf16x8e __attribute__((ext_vector_type(8), aligned(2)));
 
 // The lambdas' arguments are constants and registers: a call left in place would put those in memory.
 #define INLINE __attribute__((always_inline))
@@ -61,8 +64,7 @@ __device__ __forceinline__ void retire() {
 }
 
 template <int RB, int TB, int WA, int WB, int KS, int BUFS, int SETS, bool EARLY>
-__global__ __launch_bounds__(64 * WA * WB, 2) void k_int8_tile(Int8Gemm A, uint32_t row_tiles, uint32_t token_tiles,
-                                                              int vec) {
+__global__ __launch_bounds__(64 * WA * WB, 2) void k_int8_tile(Int8Gemm A, uint32_t row_tiles, uint32_t token_tiles) {
   constexpr int NW = WA * WB;
   constexpr int TR = 16 * RB * WA, TT = 16 * TB * WB;  // rows and tokens of a tile
   constexpr int WR = 16 * RB;                          // rows of a wave
@@ -221,7 +223,9 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_int8_tile(Int8Gemm A, uint3
   for (int s = 1; s < stages; ++s) stage.template operator()<false>(s);
 
   // A wave's sums, 16 tokens at a time, through a part of LDS of its own to rows of Y: as they are on the way
-  // in, and in a loop on the way out, a lane its eight rows of every 512 / WR-th token.
+  // in, and in a loop on the way out, a lane its eight rows of every 512 / WR-th token.  A wave's LDS accesses are done
+  // in their order; the compiler, to which lanes are strangers, is held to it.
+  auto in_order = [] INLINE { asm volatile("" ::: "memory"); };
   retire<0>();
   char* mine = lds + wave * 16 * LD;
   const int64_t left = A.rows - wave_r0 - own;
@@ -231,47 +235,29 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_int8_tile(Int8Gemm A, uint3
   for (int j = 0; j < TB; ++j) {
 #pragma unroll
     for (int i = 0; i < RB; ++i) *reinterpret_cast<i32x4*>(mine + col * LD + 4 * (16 * i + 4 * part)) = acc[i][j];
+    in_order();
     const int first = 16 * (TB * wt + j);
 #pragma unroll 1
     for (int k = lane / (WR / 8); k < 16; k += 512 / WR) {
       const int tk = first + k;
-      i32x4* sums = reinterpret_cast<i32x4*>(mine + k * LD + 4 * own);
+      const i32x4* sums = reinterpret_cast<const i32x4*>(mine + k * LD + 4 * own);
       const i32x4 lo = sums[0], hi = sums[1];
+      if (tk >= tokens || left <= 0) continue;
       f32x8i y;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         y[e] = int8_value(e < 4 ? lo[e] : hi[e - 4], zero[e], token_sum[tk], token_scale[tk], scale[e]);
-      if (!vec) {  // back, for stores of single elements side by side
-#pragma unroll
-        for (int e = 0; e < 8; ++e) reinterpret_cast<float*>(sums)[e] = y[e];
-      } else if (tk < tokens && left > 0) {
-        char* to = y0 + ((int64_t)tk * A.ldy + own) * size;
-        if (left < 8) {
-          for (int e = 0; e < left; ++e) int8_store(to, e, y[e], A.bf16);
-        } else if (A.bf16) {
-          *reinterpret_cast<bf16x8*>(to) = __builtin_convertvector(y, bf16x8);
-        } else {
-          *reinterpret_cast<f32x8i*>(to) = y;
-        }
+      char* to = y0 + ((int64_t)tk * A.ldy + own) * size;
+      if (left < 8) {
+        for (int e = 0; e < left; ++e) int8_store(to, e, y[e], A.bf16);
+      } else if (A.bf16) {
+        *reinterpret_cast<bf16x8e*>(to) = __builtin_convertvector(y, bf16x8);
+      } else {
+        reinterpret_cast<f32x4e*>(to)[0] = (f32x4e){y[0], y[1], y[2], y[3]};
+        reinterpret_cast<f32x4e*>(to)[1] = (f32x4e){y[4], y[5], y[6], y[7]};
       }
     }
-    if (!vec) {
-      constexpr int ROUND = WR / 4 < 8 ? WR / 4 : 8;  // reads on their way together
-#pragma unroll 1
-      for (int n = 0; n < 16 * WR; n += 64 * ROUND) {
-        float y[ROUND];
-#pragma unroll
-        for (int u = 0; u < ROUND; ++u) {
-          const int k = (n + 64 * u + lane) / WR, r = (n + 64 * u + lane) % WR;
-          y[u] = *reinterpret_cast<const float*>(mine + k * LD + 4 * r);
-        }
-#pragma unroll
-        for (int u = 0; u < ROUND; ++u) {
-          const int tk = first + (n + 64 * u + lane) / WR, r = (n + 64 * u + lane) % WR;
-          if (tk < tokens && wave_r0 + r < A.rows) int8_store(y0, (int64_t)tk * A.ldy + r, y[u], A.bf16);
-        }
-      }
-    }
+    in_order();
   }
 }
 
@@ -279,10 +265,8 @@ template <int RB, int TB, int WA, int WB, int KS, int BUFS, int SETS, bool EARLY
 hipError_t launch(const Int8Gemm& a, hipStream_t stream) {
   constexpr int TR = 16 * RB * WA, TT = 16 * TB * WB;
   const uint32_t rt = (uint32_t)((a.rows + TR - 1) / TR), tt = (uint32_t)((a.x.tokens + TT - 1) / TT);
-  const int size = a.bf16 ? 2 : 4;
-  const int vec = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.ldy * size % 16 == 0;
   const uint32_t grid = (rt * tt + 7) / 8 * 8;
-  k_int8_tile<RB, TB, WA, WB, KS, BUFS, SETS, EARLY><<<grid, 64 * WA * WB, 0, stream>>>(a, rt, tt, vec);
+  k_int8_tile<RB, TB, WA, WB, KS, BUFS, SETS, EARLY><<<grid, 64 * WA * WB, 0, stream>>>(a, rt, tt);
   return hipGetLastError();
 }
 
