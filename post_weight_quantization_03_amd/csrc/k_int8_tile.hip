@@ -277,6 +277,7 @@ hipError_t int8_tile_launch(const Int8Gemm& a, Int8Form form, hipStream_t stream
     case Int8Form::T256x256: return launch<8, 4, 2, 4, 64, 4, 1, false>(a, stream);
     case Int8Form::T256x128: return launch<4, 4, 4, 2, 128, 3, 2, true>(a, stream);
     case Int8Form::T128x64: return launch<4, 2, 2, 2, 128, 3, 2, true>(a, stream);
+    case Int8Form::T64x128: return launch<2, 4, 2, 2, 128, 2, 2, true>(a, stream);
     case Int8Form::T64x64: return launch<2, 2, 2, 2, 256, 3, 4, true>(a, stream);
     case Int8Form::T32x32: return launch<1, 2, 2, 1, 256, 4, 4, true>(a, stream);
     default: return launch<1, 1, 2, 1, 256, 4, 4, true>(a, stream);

@@ -106,7 +106,8 @@ SIZES = [(1, 1, 4), (1, 16, 128), (2, 17, 60), (3, 15, 64), (1, 300, 68), (15, 3
          (256, 256, 256), (257, 513, 516), (300, 40, 11008), (511, 1023, 644), (700, 260, 2048), (1, 4099, 4100),
          (5, 11008, 1024), (1000, 1000, 1000), (2, 64, 65536), (130, 40, 65536), (1025, 3, 36),
          # the larger tiles, and few tokens of many rows
-         (4000, 4001, 260), (4096, 4096, 256), (2050, 3001, 388), (1900, 2600, 1156), (1100, 2000, 516), (700, 2050, 1284),
+         (4000, 4001, 260), (4096, 4096, 256), (2050, 3001, 388), (1900, 2600, 1156), (1100, 2000, 516),
+         (700, 2050, 1284), (777, 5001, 516), (900, 3301, 1028),
          (1000, 1500, 132), (600, 900, 260), (9, 11008, 1028), (16, 9000, 260), (17, 8300, 132)]
 
 

@@ -81,7 +81,7 @@ def faults(loop, lpw, outstanding):
 
 def test_every_stage_is_retired_by_its_count(tmp_path):
     found = {n: b for n, b in kernels(asm("k_int8_tile.hip", tmp_path)).items() if FORM.search(n)}
-    assert len(found) == 6
+    assert len(found) == 7
     for name, body in found.items():
         rb, tb, wa, wb, ks, bufs, _, early = (int(x) for x in FORM.search(name).groups())
         lpw = 16 * (rb * wa + tb * wb) * ks // 1024 // (wa * wb)
