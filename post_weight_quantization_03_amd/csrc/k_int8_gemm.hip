@@ -8,13 +8,13 @@ namespace {
 // CUs, `held` each): `round` + stages * t, where a stage takes t0 while the round fills at most `knee` of the
 // places and t1 when it fills all.  The numbers fit what was measured from 300 x 512 x 512 to 8192^3; tokens x
 // columns x rows, us by form (the one that the rule takes last):
-//   4096 x 4096 x 11008  256x128 206, 256x256 193
-//   4096 x 11008 x 4096  256x128 177, 256x256 170
-//   2048 x 4096 x 4096   256x256 51, 128x64 48, 256x128 38
-//   1000 x 4096 x 4096   256x128 31, 128x64 26
-//   777 x 2052 x 5001    256x128 21.9, 128x64 26.4, 64x128 20.4
-//   500 x 4096 x 4096    64x64 20, 256x128 29, 128x64 17
-//   256 x 4096 x 4096    128x64 16, 32x32 17, 64x64 11
+//   4096 x 4096 x 11008  256x128 190, 256x256 177
+//   4096 x 11008 x 4096  256x128 166, 256x256 160
+//   2048 x 4096 x 4096   256x256 48, 128x64 45, 256x128 35
+//   1000 x 4096 x 4096   256x128 28, 64x128 25.4, 128x64 24.8
+//   777 x 2052 x 5001    256x128 21.4, 128x64 24.6, 64x128 20
+//   500 x 4096 x 4096    64x64 20, 256x128 27, 128x64 15
+//   256 x 4096 x 4096    128x64 14, 32x32 17, 64x64 11
 //   128 x 4096 x 4096    128x64 15, 64x64 10.3, 32x32 9.6
 //   64 x 4096 x 4096     64x64 9.9, 32x32 8.0
 //   1000 x 1000 x 1000   128x64 7.9, 32x32 10, 64x64 6.4
@@ -25,9 +25,9 @@ struct Form {
   float round, t0, t1, knee;
 };
 constexpr Form FORMS[] = {
-    {Int8Form::T256x256, 256, 256, 64, 1, 6.0f, 0.58f, 0.93f, 0.0f},
-    {Int8Form::T256x128, 256, 128, 128, 1, 4.0f, 0.62f, 0.95f, 0.0f},
-    {Int8Form::T128x64, 128, 64, 128, 2, 4.0f, 0.32f, 0.62f, 0.5f},
+    {Int8Form::T256x256, 256, 256, 64, 1, 6.0f, 0.55f, 0.87f, 0.0f},
+    {Int8Form::T256x128, 256, 128, 128, 1, 4.0f, 0.62f, 0.92f, 0.0f},
+    {Int8Form::T128x64, 128, 64, 128, 2, 4.0f, 0.28f, 0.58f, 0.5f},
     {Int8Form::T64x128, 64, 128, 128, 3, 3.5f, 0.50f, 0.92f, 0.33f},
     {Int8Form::T64x64, 64, 64, 256, 1, 3.5f, 0.36f, 0.39f, 0.0f},
     {Int8Form::T32x32, 32, 32, 256, 2, 2.5f, 0.21f, 0.32f, 0.5f},

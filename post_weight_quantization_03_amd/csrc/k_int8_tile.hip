@@ -11,13 +11,15 @@
 // follow each other without a pause.  EARLY: a stage's buffer has then been read (a wait for the wave's own reads goes
 // before the barrier), and the stage BUFS on is brought into it at once; else that waits for a stage.
 //
-// Measured (tokens x columns x rows): 4096 x 11008 x 4096 170 us (2.18 POP/s, 256 x 256 tiles), a library's
-// product of the same operands 161.  What bounds it is power: 58 % of the matrix cores' cycles at 1.69 GHz, and with
-// operands of zeros the same cycles at 2.27 GHz.  So products of 16 x 16 (169.8 us), which move half as many sums as
-// those of 32 x 32 (180), and no pipeline that only saves cycles (177 to 180 with any of four).  Requests of 128
-// bytes of a row: with 64-byte ones tiles of 256 x 128 took 211 us instead of 177 (256 x 256 has no room in LDS for
-// them).  Small tiles are bound by the stage's chain of wait, barrier and LDS reads (0.2 to 0.4 us), so theirs are
-// 256 columns (64 x 4096 x 4096: 8.0 us, with 128 9.5).
+// Measured (tokens x columns x rows): 4096 x 11008 x 4096 160 us (2.31 POP/s, 256 x 256 tiles), a library's
+// product of the same operands 152 to 161; 8192^3 455 us (2.42), 440 to 462.  What bounds it is power: the matrix
+// cores are busy for 58 % of the cycles at 1.69 GHz, and with operands of zeros as long at 2.27 GHz.  So, for that
+// case: products of 16 x 16 (170 us), which move half as many sums as those of 32 x 32 (180); no bank conflicts
+// (164); waves of few rows and many tokens, as rows have to be made signed (160); and nothing by a pipeline that
+// only saves cycles (177 to 180 with any of four, before these).  Requests of 128 bytes of a row: with 64-byte ones
+// tiles of 256 x 128 took 211 us instead of 177 (256 x 256 has no room in LDS for them).  Small tiles are bound by
+// the stage's chain of wait, barrier and LDS reads (0.2 to 0.4 us), so theirs are 256 columns (64 x 4096 x 4096:
+// 8.0 us, with 128 9.5).
 #include "int8.h"
 
 namespace gptq {
@@ -98,9 +100,11 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_int8_tile(Int8Gemm A, uint3
   Stream ws{reinterpret_cast<uint64_t>(A.packed) + r0 * cols, rows * cols};
   Stream xs{reinterpret_cast<uint64_t>(A.x.codes) + t0 * A.x.stride, tokens * A.x.stride};
 
-  // Piece p of a row is at place p ^ (..): rows of 64 bytes share the banks by fours, of 128 by twos.
+  // Piece p of a row is at place p ^ (..): rows of 64 bytes share the banks by fours, of 128 by twos.  The 16 lanes
+  // that are served at a time are 0 to 3, 12 to 15, 20 to 27 and so on, in two pieces: with row / 4 % 4 itself rows 0
+  // and 4 met in a bank (67 thousand of 375 thousand cycles counted as conflicts).
   auto place = [&](int row, int piece) INLINE {
-    return 16 * (piece ^ (KS == 64 ? row >> 2 & 3 : KS == 128 ? row >> 1 & 7 : row & 15));
+    return 16 * (piece ^ (KS == 64 ? -(row >> 2) & 3 : KS == 128 ? row >> 1 & 7 : row & 15));
   };
   // Lane l of load i brings the piece that belongs at place l % PIECES of row PER (..) + l / PIECES.  Tokens are padded
   // with zeros to a multiple of 128 columns; of a stage of 256 that goes past that (cut) the second half is left
@@ -274,9 +278,9 @@ hipError_t launch(const Int8Gemm& a, hipStream_t stream) {
 
 hipError_t int8_tile_launch(const Int8Gemm& a, Int8Form form, hipStream_t stream) {
   switch (form) {
-    case Int8Form::T256x256: return launch<8, 4, 2, 4, 64, 4, 1, false>(a, stream);
-    case Int8Form::T256x128: return launch<4, 4, 4, 2, 128, 3, 2, true>(a, stream);
-    case Int8Form::T128x64: return launch<4, 2, 2, 2, 128, 3, 2, true>(a, stream);
+    case Int8Form::T256x256: return launch<4, 8, 4, 2, 64, 4, 1, false>(a, stream);
+    case Int8Form::T256x128: return launch<2, 8, 8, 1, 128, 3, 2, true>(a, stream);
+    case Int8Form::T128x64: return launch<2, 4, 4, 1, 128, 3, 2, true>(a, stream);
     case Int8Form::T64x128: return launch<2, 4, 2, 2, 128, 2, 2, true>(a, stream);
     case Int8Form::T64x64: return launch<2, 2, 2, 2, 256, 3, 4, true>(a, stream);
     case Int8Form::T32x32: return launch<1, 2, 2, 1, 256, 4, 4, true>(a, stream);
