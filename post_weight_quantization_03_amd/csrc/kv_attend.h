@@ -27,7 +27,9 @@ __device__ __forceinline__ float value_exponent(float scale) {
 // head's group: row r is token r / group, head r % group.
 // MASKED: the first tokens that stay visible, up to a multiple of 64 (head), and the window follow each other
 // without what lies between: the span counts from 0, and count v stands for token v + (v >= head ? gap : 0).
-// Blocks are looked up only for tokens below `sinks` and from `lo` on.
+// Blocks are looked up only for tokens below `sinks` and from `lo` on.  The head costs a tile of 64 tokens however few
+// are visible in it: a prompt of 8195 tokens with a window of 1024 (18 tiles a workgroup) takes 205 us with 4 first
+// tokens and 189 without; one token of each of 16 sequences over a window of 4096, 37 us with the join.
 struct Span {
   int64_t begin, end;
   int head, gap, sinks, lo;
@@ -83,7 +85,9 @@ __device__ __forceinline__ Sees row_sees(const KvAttention& A, const Seq& s, int
 }
 
 // MASKED: tokens from lo to hi - 1 and below sinks (and hi) are seen by the row, and of the new tokens, from
-// hi = before on, those of its mask.
+// hi = before on, those of its mask.  A word of 64 bits is made of that for a row and tile of which not all is seen
+// (the mask's two words are read then); other tiles take the plain path.  With a tree of 64 tokens over 16 sequences of
+// 8192 the call takes what the causal one does, 171 us.
 struct RowMask {
   int lo, hi, sinks;
   const uint64_t* words;  // null without a tree
