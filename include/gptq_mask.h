@@ -54,7 +54,8 @@ int gptq_kv_masked_attention(const gptq_kv_cache* cache, const gptq_kv_batch* ba
  *   tree uint64 [total][tree_stride]      words 0 .. ceil(max_new / 64) - 1: the new tokens on
  *        that path and itself, those at positions that `window` and `sinks` leave visible
  * positions are those for gptq_qk_norm_rope and for gptq_kv_mask.  A parent out of range is raised and
- * taken for -1; kv_len < n_b is raised and the sequence's rows are left.  The batch's block_table is not used. */
+ * taken for -1; kv_len < n_b is raised and the sequence's rows are left.  The outputs must not overlap the inputs.
+ * The time grows with the longest path (a chain of 8192: 67 us).  The batch's block_table is not used. */
 int gptq_kv_tree(const gptq_kv_batch* batch, const int32_t* parents, int64_t window, int64_t sinks,
                  int32_t* positions, uint64_t* tree, int64_t tree_stride, int32_t* d_status, gptq_stream_t stream);
 

@@ -19,6 +19,8 @@ Modules
               quantized-model inputs, before GPTQ.
   attn_ref    the attention operators: per-head norm and position rotation with
               their gradients, the paged 8-bit cache, attention over it.
+  int8_ref    tokens to 8-bit codes and their integer product with a layer.
+  mask_ref    what rows see by window, first tokens and trees of new tokens.
 
 Parity pins: every function here is checked in ``tests/test_oracle_*.py``
 against closed forms, the hand-worked 4x8 example in ``tests/golden``,

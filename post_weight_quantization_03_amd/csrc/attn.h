@@ -79,6 +79,8 @@ bool kv_attention_fits(const gptq_kv_cache& cache, const gptq_kv_batch& batch, b
                        int64_t sinks);
 hipError_t kv_attention(const KvAttention& a, hipStream_t stream);
 
+// Whether the launch stays within the grid's limits.
+bool kv_tree_fits(const gptq_kv_batch& b);
 hipError_t kv_tree(const gptq_kv_batch& b, const int32_t* parents, int64_t window, int64_t sinks, int32_t* positions,
                    uint64_t* tree, int64_t stride, int32_t* d_status, hipStream_t stream);
 

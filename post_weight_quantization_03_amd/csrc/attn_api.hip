@@ -352,7 +352,7 @@ int gptq_kv_tree(const gptq_kv_batch* batch, const int32_t* parents, int64_t win
       !aligned(batch->kv_len, 4) || !aligned(parents, 4) || !aligned(positions, 4) || !aligned(tree, 8) ||
       parents == positions)
     return GPTQ_EINVAL;
-  if (batch->batch > MAX_GRID) return GPTQ_EUNSUPPORTED;
+  if (!kv_tree_fits(*batch)) return GPTQ_EUNSUPPORTED;
   return kv_tree(*batch, parents, window, sinks, positions, tree, tree_stride, d_status, (hipStream_t)stream) ==
                  hipSuccess
              ? GPTQ_OK

@@ -312,6 +312,26 @@ def test_tree_masks(new, lengths, mask):
     assert np.array_equal(out.positions.cpu().numpy(), want_p) and np.array_equal(words.cpu().numpy(), want_w)
 
 
+@pytest.mark.parametrize("before", [0, 3, 200])
+@pytest.mark.parametrize("mask", [(0, 0), (1, 0), (70, 5), (64, 64), (3, 130), (130, 1), (129, 300), (500, 9)])
+def test_masks_of_long_paths(before, mask):
+    """Chains over several words, with gaps, cut by window and first tokens inside and between words."""
+    import post_weight_quantization_03_amd as g
+    rng = np.random.default_rng(59)
+    chain = np.arange(-1, 319)
+    gaps = np.maximum(np.arange(320) - rng.integers(1, 4, 320), -1)
+    far = np.where(np.arange(320) % 65 == 64, np.arange(320) - 64, chain)
+    start = np.arange(0, 961, 320, dtype=np.int32)
+    batch = g.KVBatch(to_dev(start), to_dev(np.full(3, before + 320, np.int32)), to_dev(np.zeros((3, 8), np.int32)),
+                      960, 320, before + 320)
+    got = g.gptq_kv_tree(batch, to_dev(np.concatenate([chain, gaps, far]).astype(np.int32)), *mask)
+    for b, parents in enumerate((chain, gaps, far)):
+        at, among = M.tree(parents, before, *mask)
+        rows = slice(start[b], start[b + 1])
+        assert np.array_equal(got.positions[rows].cpu().numpy(), at)
+        assert np.array_equal(got.mask[rows].cpu().numpy(), M.words(among, 5).view(np.int64))
+
+
 @pytest.mark.parametrize("mask", [(0, 0), (300, 5)])
 def test_a_long_chain_of_drafts(mask):
     """More tokens than fit in LDS."""

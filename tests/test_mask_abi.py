@@ -120,6 +120,8 @@ def test_tree_refusals():
                 dict(b=attn.gptq_kv_batch(A, None, A, 5, 2, 8, 4, 300))):
         assert tree(**bad) == E
     assert tree(batch(n=1 << 24, total=1 << 24)) == U
+    assert tree(batch(n=1 << 16, total=1 << 20, max_new=256 * 256 + 1), stride=1025) == U
+    assert tree(batch(total=1 << 25, max_new=65535 * 256 + 1), stride=1 << 18) == U
 
 
 def binding_arguments(odd=None):
