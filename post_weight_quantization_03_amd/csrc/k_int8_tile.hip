@@ -19,7 +19,9 @@
 // only saves cycles (177 to 180 with any of four, before these).  Requests of 128 bytes of a row: with 64-byte ones
 // tiles of 256 x 128 took 211 us instead of 177 (256 x 256 has no room in LDS for them).  Small tiles are bound by
 // the stage's chain of wait, barrier and LDS reads (0.2 to 0.4 us), so theirs are 256 columns (64 x 4096 x 4096:
-// 8.0 us, with 128 9.5).
+// 8.0 us, with 128 9.5), and by what the CUs read out of the L2s, 15 to 20 TB/s: with twice the waves, each half of
+// them at half of the columns, products of up to 256 tiles take 3 to 8 % less and larger ones up to 30 % more (not
+// kept).
 #include "int8.h"
 
 namespace gptq {
