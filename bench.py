@@ -37,9 +37,9 @@ PEAK_HBM_GBS = 8000.0
 # the summary with the commands is profiles/hbm_counters_q_proj_4096x4096_262144tok.md.  Valid
 # only for the kernel sources they were taken on (k_hessian.hip and the work decomposition it
 # includes, syrk_plan.h): different sources report null.
-SYRK_TRAFFIC = {"sources_sha256": "9daeb3705703cd2709aba5e44ec8439a48e329726251bfc3a4ed44f8da19812d",
+SYRK_TRAFFIC = {"sources_sha256": "8952fbf7191d791ea96c51eeffa863712a8eb695bbba17f28e1574468b8b3e5f",
                 "workload": "q_proj_4096", "tokens": 262144,
-                "fetch_bytes": 9207598266.6, "write_bytes": 492690001.3}
+                "fetch_bytes": 9207576928.4, "write_bytes": 492600896.0}
 SYRK_SOURCES = ("k_hessian.hip", "syrk_plan.h")
 
 

@@ -20,6 +20,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ int acc_row(int r, int lane) { return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); }
 __device__ __forceinline__ int acc_col(int lane) { return lane & 31; }
 
+// A direct load: 16 bytes a lane from base + off to LDS, lane 0's at lds.  Issued from asm where every wait on these
+// loads is an explicit counted s_waitcnt, which the compiler's wait insertion must not see.  It does not look
+// inside asm for the wait state that the hardware asks for between a write of M0 and a direct load either (without
+// it a piece may land in the place of the load before, and its own keeps what was there), so the s_nop is part of it.
+__device__ __forceinline__ void direct_load(uint32_t off, const char* base, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds));
+}
+
 // Device status codes are gptq_status values; kernels raise them with atomicMax.
 __device__ __forceinline__ void raise_status(int* st, int code) { atomicMax(st, code); }
 

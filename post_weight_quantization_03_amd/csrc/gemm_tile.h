@@ -78,7 +78,7 @@ __device__ __forceinline__ void dma_issue(DmaOp<TM>& d, char* dst, int wave) {
 #pragma unroll
   for (int i = 0; i < Geo<TM>::LPW; ++i) {
     const uint32_t lds = (uint32_t)(uintptr_t)(lds_char*)(dst + (wave * Geo<TM>::LPW + i) * 1024);
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(d.off[i]), "s"(d.base), "{m0}"(lds));
+    direct_load(d.off[i], d.base, lds);
   }
   uint64_t b = reinterpret_cast<uint64_t>(d.base) + (uint64_t)d.step;
   asm volatile("" : "+s"(b));

@@ -259,7 +259,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 __device__ __forceinline__ void dma_piece(const DirectSrc& d, char* buf, int wave, int i) {
   const int r0 = (KB / 4) * wave + 2 * i;
   const uint32_t lds = (uint32_t)(uintptr_t)(lds_char*)(buf + r0 * ROWB);
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(d.off[i]), "s"(d.base), "{m0}"(lds));
+  direct_load(d.off[i], d.base, lds);
 }
 __device__ __forceinline__ void dma_advance(DirectSrc& d, int64_t stage_step) {
   uint64_t b = reinterpret_cast<uint64_t>(d.base) + (uint64_t)(stage_step * 2);
@@ -274,7 +274,7 @@ __device__ __forceinline__ void stage_direct(DirectSrc& d, char* buf, int wave, 
     const int r0 = (KB / 4) * wave + 2 * i;
     if constexpr (ASM) {
       const uint32_t lds = (uint32_t)(uintptr_t)(lds_char*)(buf + r0 * ROWB);
-      asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(d.off[i]), "s"(d.base), "{m0}"(lds));
+      direct_load(d.off[i], d.base, lds);
     } else {
       __builtin_amdgcn_global_load_lds(d.base + d.off[i], (lds_void*)(buf + r0 * ROWB), 16, 0, 0);
     }

@@ -55,8 +55,9 @@ struct Stream {
   }
 };
 
+// With the wait state between the write of M0 and a load that uses it, as in direct_load.
 __device__ __forceinline__ void load_to_lds(uint32_t offset, u32x4s buffer, uint32_t lds) {
-  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer), "{m0}"(lds));
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer), "{m0}"(lds));
 }
 
 // All but the wave's N newest loads have come, in every wave.

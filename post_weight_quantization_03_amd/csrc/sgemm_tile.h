@@ -123,14 +123,14 @@ __device__ __forceinline__ void sdma_issue(const SplitGemm& g, const SDma& d, in
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t la = (uint32_t)(uintptr_t)(lds_char*)(buf + (wave * 2 + i) * 1024);
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(d.a_off[i]), "s"(ab), "{m0}"(la));
+    direct_load(d.a_off[i], ab, la);
   }
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     const int plane = __builtin_amdgcn_readfirstlane(d.b_plane[i]);
     const char* bb = uniform_ptr(g.B[plane] + (int64_t)k0 * g.ldb + n0);
     const uint32_t lb = (uint32_t)(uintptr_t)(lds_char*)(buf + __builtin_amdgcn_readfirstlane(d.b_dst[i]));
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(d.b_off[i]), "s"(bb), "{m0}"(lb));
+    direct_load(d.b_off[i], bb, lb);
   }
 }
 
