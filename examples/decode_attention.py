@@ -187,17 +187,21 @@ def decode(block, prompt, steps, graph=True):
     return first, torch.stack(outs)
 
 
+def half_tree(drafts):
+    """Parents of a tree of `drafts` tokens, each token after its half, and the path to its last, a deepest one."""
+    parents = [(i + 1) // 2 - 1 for i in range(drafts)]
+    path, at = [], drafts - 1
+    while at >= 0:
+        path.insert(0, at)
+        at = parents[at]
+    return parents, path
+
+
 def check_drafts(batch, prompt, drafts, rounds=8):
-    """Times rounds of a tree of `drafts` tokens a sequence (each token after its half) of which the longest
-    path is kept."""
+    """Times rounds of a tree of `drafts` tokens a sequence of which the longest path is kept."""
     block = DraftBlock(batch=batch, max_tokens=prompt + (rounds + 1) * drafts, window=1024, sinks=4)
-    parents = torch.arange(drafts, dtype=torch.int32, device=block.device).expand(batch, drafts)
-    parents = torch.div(parents + 1, 2, rounding_mode="floor") - 1
-    path = []
-    while drafts:
-        path.insert(0, drafts - 1)
-        drafts = (drafts + 1) // 2 - 1 if drafts > 1 else 0
-    path = torch.tensor(path, device=block.device).expand(batch, -1)
+    parents, path = (torch.tensor(t, dtype=torch.int32, device=block.device).expand(batch, -1)
+                     for t in half_tree(drafts))
     block.extend(torch.randn((batch, prompt, block.hidden), device=block.device))
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for i in range(rounds + 1):
