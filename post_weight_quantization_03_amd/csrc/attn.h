@@ -69,7 +69,7 @@ struct KvAttention {
   int bf16, vec;
   void* workspace;
   int32_t* d_status;
-  int masked;         // with visible first tokens or a tree; else mask is not looked at
+  int masked;         // with a mask's window or a tree; else mask is not looked at
   gptq_kv_mask mask;  // sinks 0 without a window
 };
 size_t kv_attention_workspace(const gptq_kv_cache& cache, const gptq_kv_batch& batch, bool bf16,

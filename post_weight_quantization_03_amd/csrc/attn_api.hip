@@ -313,7 +313,8 @@ static int attend(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const 
   a.vec = vec_ok(q, q_token, q_head, dtype) && vec_ok(out, out_token, out_head, dtype);
   a.workspace = workspace;
   a.d_status = d_status;
-  a.masked = tree || sinks > 0;
+  // a window without first tokens too: the plain kernels look up the blocks of a whole tile at its edge
+  a.masked = tree || (mask && seen.window > 0);
   if (a.masked) a.mask = *mask;
   a.mask.sinks = sinks;
   return kv_attention(a, (hipStream_t)stream) == hipSuccess ? GPTQ_OK : GPTQ_EHIP;
