@@ -155,6 +155,25 @@ def _given(name, t, device):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _tangent(torch, *tensors):
+    """Whether forward-mode differentiation goes through one of the tensors (whatever no_grad says)."""
+    ad = torch.autograd.forward_ad
+    return (ad._current_level >= 0 and not torch.is_inference_mode_enabled()
+            and any(ad.unpack_dual(t).tangent is not None for t in tensors if t is not None))
+
+
+def _refuse_gradients(what, torch, *tensors):
+    """Refuses what an operator without derivatives would cut off from its inputs."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise ValueError(f"{what} has no gradients: call it under torch.no_grad() or on detached tensors")
+    _refuse_tangents(what, torch, *tensors)
+
+
+def _refuse_tangents(what, torch, *tensors):
+    if _tangent(torch, *tensors):
+        raise ValueError(f"{what} has no gradients in forward mode: call it on detached tensors")
+
+
 def _apart(device, *handles):
     """The error of a handle whose tensors are not on the call's device."""
     h = next(h for h in handles if h.device != device)
@@ -363,11 +382,13 @@ def gptq_qk_norm_rope(q, k, positions, rope: Rope, q_weight=None, k_weight=None,
     """(q_out, k_out): RMS norm (where a weight [dim] is given) and rotation of every head of
     q and k [tokens, heads, dim] (bf16 or fp32) at positions [tokens] (int32).  q or k may be None;
     q_out may be q.  Where autograd records and q, k or a weight requires gradients, the outputs carry
-    them (weights' gradients rounded to the weight's type); q_out, k_out and stream are then refused."""
+    them (weights' gradients rounded to the weight's type); q_out, k_out and stream are then refused,
+    and so are inputs of forward-mode differentiation."""
     like = q if q is not None else k
     if like is None:
         raise ValueError("q or k must be given")
     torch = _g._torch()
+    _refuse_tangents("norm and rotation", torch, q, k, q_weight, k_weight)
     if torch.is_grad_enabled() and (like.requires_grad or k is not None and k.requires_grad or
                                     q_weight is not None and q_weight.requires_grad or
                                     k_weight is not None and k_weight.requires_grad):
@@ -534,8 +555,13 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
     """Attention of the batch's new tokens q [total, q_heads, dim] (bf16 or fp32) over the cache.
     sm_scale: dim^-1/2 unless given.  sinks: first tokens that the window leaves visible.  tree: the new
     tokens see those of their masks, and what was before them.  Returns out, or (out, lse) when lse
-    [total, q_heads] (fp32) is given or wanted.  Rows that no sequence owns are left as they are."""
+    [total, q_heads] (fp32) is given or wanted.  Rows that no sequence owns are left as they are.
+    Outputs carry no gradients; with sinks or a tree a q that requires them is refused."""
     torch = _g._torch()
+    if sinks or tree is not None:
+        _refuse_gradients("attention over the cache", torch, q)
+    else:
+        _refuse_tangents("attention over the cache", torch, q)
     device = q.get_device()
     raw = _raw_stream(torch, device, stream)
     if raw is None:

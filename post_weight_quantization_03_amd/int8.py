@@ -4,7 +4,8 @@ scale each, and their product with a layer of 8-bit codes with one scale and zer
 ``Tokens`` holds quantized tokens together with the C struct built from them once; several layers may
 share them.  The functions carry the C names, marshal arguments, and raise ``GptqError`` on a non-zero
 status.  A call is made on the device of its tensors, and a call on another ``stream`` allocates what
-it needs from that stream.  They are for serving: inputs that require gradients are refused.
+it needs from that stream.  They are for serving: inputs that require gradients, or carry them in
+forward mode, are refused.
 """
 
 from __future__ import annotations
@@ -12,7 +13,7 @@ from __future__ import annotations
 import ctypes
 
 import post_weight_quantization_03_amd as _g
-from .attn import _apart, _elsewhere, _empty, _one_device, _raw_stream
+from .attn import _apart, _elsewhere, _empty, _one_device, _raw_stream, _refuse_gradients
 
 _vp, _i64 = ctypes.c_void_p, ctypes.c_int64
 
@@ -95,20 +96,15 @@ def _matrix(name, t, device):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # a single row may carry any stride
 
 
-def _refuse_gradients(torch, *tensors):
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        raise ValueError("the 8-bit product has no gradients: call it under torch.no_grad() or on detached tensors")
-
-
 def gptq_quantize_tokens(X, out: Tokens = None, stream=None) -> Tokens:
     """Codes, scales and sums of X [tokens, cols] (bf16 or fp32, unit column stride), new ones or `out`."""
     torch = _g._torch()
+    _refuse_gradients("rounding tokens to 8 bits", torch, X)
     device = X.get_device()
     raw = _raw_stream(torch, device, stream)
     if raw is None:
         with torch.cuda.device(device):
             return gptq_quantize_tokens(X, out, stream)
-    _refuse_gradients(torch, X)
     ldx = _matrix("X", X, device)
     tokens, cols = X.shape
     if out is None:
@@ -127,6 +123,7 @@ def gptq_int8_gemm(packed, scales, zeros, x: Tokens, Y=None, dtype=None, stream=
     """Y [tokens, rows] (bf16 unless `dtype` or Y says fp32) = the tokens through the layer of packed
     [rows, cols / 4] 8-bit codes (int32 words), scales fp32 and zeros uint8 [rows] or [rows, 1]."""
     torch = _g._torch()
+    _refuse_gradients("the 8-bit product", torch, scales)
     device = packed.get_device()
     raw = _raw_stream(torch, device, stream)
     if raw is None:
@@ -137,7 +134,6 @@ def gptq_int8_gemm(packed, scales, zeros, x: Tokens, Y=None, dtype=None, stream=
             raise _elsewhere(name, t, device)
     if x.device != device:
         raise _apart(device, x)
-    _refuse_gradients(torch, scales)
     rows = packed.shape[0]
     if (packed.dim() != 2 or packed.element_size() != 4 or packed.shape[1] * 4 != x.cols
             or scales.dtype != torch.float32 or zeros.dtype != torch.uint8 or scales.numel() != rows
