@@ -322,6 +322,12 @@ class KVTree:
                    batch.kv_len.new_empty((batch.total, -(-batch.max_new // 64)), dtype=torch.int64))
 
 
+def _limits(window, sinks, batch):
+    """window and sinks as the batch's sequences meet them: (0, 0) where they limit nothing."""
+    sinks = sinks or 0
+    return (0, 0) if window == 0 or window >= batch.max_kv or sinks >= batch.max_kv else (window, sinks)
+
+
 def _check_tree(tree, batch):
     if tree.total != batch.total or 64 * tree.words < batch.max_new:
         raise ValueError("the tree must have a row for each of the batch's tokens and a bit for each new one")
@@ -596,7 +602,7 @@ def gptq_kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale=None, causal: 
             if tree.device != device:
                 raise _apart(device, tree)
             _check_tree(tree, batch)
-            if (tree.window, tree.sinks) not in ((window, sinks), (None, None)):
+            if tree.window is not None and _limits(tree.window, tree.sinks, batch) != _limits(window, sinks, batch):
                 raise ValueError(f"the tree was made for window {tree.window} and sinks {tree.sinks}")
         mask = _mask(sinks, tree)
     if workspace is None:

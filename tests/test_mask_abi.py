@@ -185,3 +185,29 @@ def test_trees_are_checked(calls):  # noqa: F811
     with pytest.raises(ValueError):
         g.KVTree(Tensor((2,), torch.int32), a["mask"])
     assert [c[0] for c in calls] == ["gptq_kv_masked_attention"]
+
+
+SAME = [((0, 4), (0, 0)), ((0, 0), (0, 7)), ((40, 0), (0, 0)), ((1 << 40, 3), (50, 5)), ((9, 40), (0, 0)),
+        ((9, 50), (8, 1 << 40)), ((9, None), (9, 0)), ((None, None), (9, 2))]
+OTHER = [((39, 0), (0, 0)), ((9, 39), (9, 38)), ((9, 39), (0, 0)), ((9, None), (9, 1)), ((9, 1), (10, 1))]
+
+
+@pytest.mark.parametrize("made_for,called_with", SAME)
+def test_limits_that_mean_the_same_are_the_same(calls, made_for, called_with):  # noqa: F811
+    """First tokens without a window, a window as long as any sequence (40) and first tokens that are all of them limit
+    nothing."""
+    a = binding_arguments()
+    for one, two in ((made_for, called_with), (called_with, made_for)):
+        if None not in two:
+            g.gptq_kv_attention(a["q"], *cached(a), out=a["out"], workspace=a["workspace"], window=two[0],
+                                sinks=two[1], tree=made(a, *one))
+            assert calls.pop()[0] == "gptq_kv_masked_attention"
+
+
+@pytest.mark.parametrize("made_for,called_with", OTHER)
+def test_limits_that_differ_are_refused(calls, made_for, called_with):  # noqa: F811
+    a = binding_arguments()
+    with pytest.raises(ValueError, match="made for"):
+        g.gptq_kv_attention(a["q"], *cached(a), out=a["out"], window=called_with[0], sinks=called_with[1],
+                            tree=made(a, *made_for))
+    assert calls == []
