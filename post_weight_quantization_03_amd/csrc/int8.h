@@ -3,6 +3,7 @@
 
 #include "common.h"
 #include "gptq_int8.h"
+#include "int8_plan.h"
 
 namespace gptq {
 
@@ -35,7 +36,6 @@ bool int8_gemm_fits(int64_t rows, int64_t cols, int64_t tokens);
 hipError_t int8_gemm(const Int8Gemm& a, hipStream_t stream);
 // k_int8_rows.hip: up to 16 tokens.  k_int8_tile.hip: tiles of rows x tokens.
 hipError_t int8_rows_launch(const Int8Gemm& a, hipStream_t stream);
-enum class Int8Form { T256x256, T256x128, T128x64, T64x128, T64x64, T32x32, T32x16 };
 hipError_t int8_tile_launch(const Int8Gemm& a, Int8Form form, hipStream_t stream);
 
 #ifdef __HIPCC__

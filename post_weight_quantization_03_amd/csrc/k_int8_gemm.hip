@@ -1,74 +1,17 @@
-// The 8-bit product: which kernel takes a call.
+// The 8-bit product: the launch of the kernel that int8_plan.h chooses.
 #include "int8.h"
 
 namespace gptq {
-namespace {
-
-// A form's time (us) is estimated as START + for every round of the workgroups that the chip holds at a time (256
-// CUs, `held` each): `round` + stages * t, where a stage takes t0 while the round fills at most `knee` of the
-// places and t1 when it fills all.  The numbers fit what was measured from 300 x 512 x 512 to 8192^3; tokens x
-// columns x rows, us by form (the one that the rule takes last):
-//   4096 x 4096 x 11008  256x128 190, 256x256 177
-//   4096 x 11008 x 4096  256x128 166, 256x256 160
-//   2048 x 4096 x 4096   256x256 48, 128x64 45, 256x128 35
-//   1000 x 4096 x 4096   256x128 28, 64x128 25.4, 128x64 24.8
-//   777 x 2052 x 5001    256x128 21.4, 128x64 24.6, 64x128 20
-//   500 x 4096 x 4096    64x64 20, 256x128 27, 128x64 15
-//   256 x 4096 x 4096    128x64 14, 32x32 17, 64x64 11
-//   128 x 4096 x 4096    128x64 15, 64x64 10.3, 32x32 9.6
-//   64 x 4096 x 4096     64x64 9.9, 32x32 8.0
-//   1000 x 1000 x 1000   128x64 7.9, 32x32 10, 64x64 6.4
-//   61 x 11008 x 4096    64x64 20, 32x16 17, 32x32 15
-struct Form {
-  Int8Form form;
-  int rows, tokens, cols, held;
-  float round, t0, t1, knee;
-};
-constexpr Form FORMS[] = {
-    {Int8Form::T256x256, 256, 256, 64, 1, 6.0f, 0.55f, 0.87f, 0.0f},
-    {Int8Form::T256x128, 256, 128, 128, 1, 4.0f, 0.62f, 0.92f, 0.0f},
-    {Int8Form::T128x64, 128, 64, 128, 2, 4.0f, 0.28f, 0.58f, 0.5f},
-    {Int8Form::T64x128, 64, 128, 128, 3, 3.5f, 0.50f, 0.92f, 0.33f},
-    {Int8Form::T64x64, 64, 64, 256, 1, 3.5f, 0.36f, 0.39f, 0.0f},
-    {Int8Form::T32x32, 32, 32, 256, 2, 2.5f, 0.21f, 0.32f, 0.5f},
-    {Int8Form::T32x16, 32, 16, 256, 3, 2.0f, 0.16f, 0.36f, 0.33f},
-};
-constexpr float START = 2.5f;
-constexpr int CUS = 256;
-
-int64_t tiles_of(const Form& f, int64_t rows, int64_t tokens) {
-  return (rows + f.rows - 1) / f.rows * ((tokens + f.tokens - 1) / f.tokens);
-}
-
-float estimate(const Form& f, int64_t rows, int64_t cols, int64_t tokens) {
-  const int64_t tiles = tiles_of(f, rows, tokens), places = (int64_t)CUS * f.held, full = tiles / places;
-  const float stages = (float)((cols + f.cols - 1) / f.cols);
-  const float filled = (float)(tiles % places) / (float)places;
-  const float over = filled > f.knee ? (filled - f.knee) / (1.0f - f.knee) : 0.0f;
-  const float last = filled > 0.0f ? f.round + stages * (f.t0 + (f.t1 - f.t0) * over) : 0.0f;
-  return START + (float)full * (f.round + stages * f.t1) + last;
-}
-
-const Form& best(int64_t rows, int64_t cols, int64_t tokens) {
-  const Form* b = &FORMS[0];
-  for (const Form& f : FORMS)
-    if (estimate(f, rows, cols, tokens) < estimate(*b, rows, cols, tokens)) b = &f;
-  return *b;
-}
-
-// Up to two workgroups a CU (k_int8_rows.hip has both sides); from 16384 rows on tiles of 32 are in the lead.
-bool by_rows(int64_t rows, int64_t tokens) { return tokens <= 16 && rows <= 8192; }
-
-}  // namespace
 
 bool int8_gemm_fits(int64_t rows, int64_t cols, int64_t tokens) {
   // at most 512 threads a workgroup
-  return by_rows(rows, tokens) || tiles_of(best(rows, cols, tokens), rows, tokens) <= ((int64_t)1 << 23) - 8;
+  return int8_by_rows(rows, tokens) ||
+         int8_tiles_of(int8_best(rows, cols, tokens), rows, tokens) <= ((int64_t)1 << 23) - 8;
 }
 
 hipError_t int8_gemm(const Int8Gemm& a, hipStream_t stream) {
-  if (by_rows(a.rows, a.x.tokens)) return int8_rows_launch(a, stream);
-  return int8_tile_launch(a, best(a.rows, a.x.cols, a.x.tokens).form, stream);
+  if (int8_by_rows(a.rows, a.x.tokens)) return int8_rows_launch(a, stream);
+  return int8_tile_launch(a, int8_best(a.rows, a.x.cols, a.x.tokens).form, stream);
 }
 
 }  // namespace gptq

@@ -6,7 +6,7 @@
 // each with three chunks on their way; their sums are added in LDS at the end (integers: in any order).
 //
 // One token (times of calls in a row): 4096 columns x 4096 rows 6.1 us, 11008 x 4096 10.3 (4.4 TB/s), where tiles of
-// 32 x 16 take 7.1 and 12.8; 4096 x 11008 12.5, where they take 10.1 (k_int8_gemm.hip goes by the rows).  With eight
+// 32 x 16 take 7.1 and 12.8; 4096 x 11008 12.5, where they take 10.1 (int8_plan.h goes by the rows).  With eight
 // waves and four chunks 6.2, 11.2 and 14.1; eight chunks 10.5, 17.3 and 20.4: fewer workgroups are resident.
 #include "int8.h"
 
