@@ -155,22 +155,19 @@ def _given(name, t, device):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _tangent(torch, *tensors):
-    """Whether forward-mode differentiation goes through one of the tensors (whatever no_grad says)."""
-    ad = torch.autograd.forward_ad
-    return (ad._current_level >= 0 and not torch.is_inference_mode_enabled()
-            and any(ad.unpack_dual(t).tangent is not None for t in tensors if t is not None))
-
-
-def _refuse_gradients(what, torch, *tensors):
-    """Refuses what an operator without derivatives would cut off from its inputs."""
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+def _refuse_gradients(what, torch, x):
+    """Refuses what an operator without derivatives would cut off from its input."""
+    if x.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{what} has no gradients: call it under torch.no_grad() or on detached tensors")
-    _refuse_tangents(what, torch, *tensors)
+    _refuse_tangents(what, torch, x)
 
 
 def _refuse_tangents(what, torch, *tensors):
-    if _tangent(torch, *tensors):
+    """Forward-mode differentiation goes through its dual tensors whatever no_grad says."""
+    ad = torch.autograd.forward_ad
+    if ad._current_level < 0 or torch.is_inference_mode_enabled():
+        return
+    if any(ad.unpack_dual(t).tangent is not None for t in tensors if t is not None):
         raise ValueError(f"{what} has no gradients in forward mode: call it on detached tensors")
 
 
