@@ -313,9 +313,9 @@ class KVTree:
 
     @classmethod
     def empty(cls, batch: KVBatch):
-        """Room for the positions and masks of a batch."""
+        """Room for the positions (0 until they are written) and masks of a batch."""
         torch = _g._torch()
-        return cls(batch.kv_len.new_empty((batch.total,)),
+        return cls(batch.kv_len.new_zeros((batch.total,)),
                    batch.kv_len.new_empty((batch.total, -(-batch.max_new // 64)), dtype=torch.int64))
 
 
@@ -627,7 +627,8 @@ def gptq_kv_tree(batch: KVBatch, parents, window: int = 0, sinks: int = 0, out: 
                  stream=None) -> KVTree:
     """Positions and masks of the batch's new tokens as trees, new ones or `out`: parents int32 [total] holds
     for each the new token of its sequence that it follows, an earlier one, or -1 for the cache's last token.
-    window and sinks: those of the attention that the tree is for."""
+    window and sinks: those of the attention that the tree is for.  Rows that no sequence has stay as they are: a
+    padded batch gives an `out` of KVTree.empty, whose positions there are 0 and can be rotated by."""
     torch = _g._torch()
     device = batch.device
     raw = _raw_stream(torch, device, stream)

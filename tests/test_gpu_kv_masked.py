@@ -501,3 +501,18 @@ def test_a_window_without_first_tokens(form, bf16):
         more["lse"] = want_lse
         bound = attention_bound(want, more, lengths[b], dim, bf16, np.abs(kv[b][1]).max(initial=0))[0]
         close(f"out[{b}]", got[rows], want, bound + 1e-38)
+
+
+def test_positions_of_a_padded_batch_can_be_rotated():
+    """Rows that no sequence has hold position 0 in the room that KVTree.empty makes."""
+    import post_weight_quantization_03_amd as g
+    torch, dev = torch_dev()
+    c = Paged(np.random.default_rng(51), [100, 40], 2, 16, 64)
+    plan, start = c.plan([5, 3], total=23)
+    torch.full((23,), -123456, dtype=torch.int32, device=dev)  # what the room may be made of
+    tree = g.gptq_kv_tree(plan, to_dev(np.full(23, -1, np.int32)), out=g.KVTree.empty(plan))
+    assert tree.positions.tolist() == [95] * 5 + [37] * 3 + [0] * 15
+    cos = torch.ones((100, 32), device=dev)
+    q, st = torch.randn((23, 2, 64), device=dev), to_dev(np.zeros(1, np.int32))
+    out = g.gptq_qk_norm_rope(q, None, tree.positions, g.Rope(cos, torch.zeros_like(cos)), d_status=st)[0]
+    assert int(st) == 0 and torch.equal(out, q)
