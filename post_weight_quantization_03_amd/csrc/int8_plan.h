@@ -60,7 +60,19 @@ inline const Int8Tiles& int8_best(int64_t rows, int64_t cols, int64_t tokens) {
   return *b;
 }
 
-// Up to two workgroups a CU (k_int8_rows.hip has both sides); from 16384 rows on tiles of 32 are in the lead.
+// Up to two workgroups of k_int8_rows.hip a CU.  Its time and that of tiles of 32 x 16, us, layers in turn that
+// together fill no cache:
+//   rows              2048          4096          6144          8192         11008         16384
+//   1 token
+//     1024 columns     3.1 / 4.3     3.2 / 4.5     4.6 / 5.0     4.7 / 5.5     5.9 / 6.8     7.1 / 7.4
+//     4096             5.6 / 7.7     6.3 / 8.2     9.0 / 9.0    10.0 / 10.0   13.6 / 13.4   17.0 / 20.2
+//     11008           10.0 / 14.7   14.2 / 16.9   20.6 / 22.7   24.2 / 26.8   34.1 / 34.3   46.6 / 45.8
+//   16 tokens
+//     1024             3.5 / 4.3     3.6 / 4.5     5.2 / 5.2     5.3 / 5.5     6.9 / 6.9     8.4 / 7.4
+//     4096             6.5 / 7.9     7.0 / 8.5    11.2 / 9.1    11.8 / 10.1   15.8 / 14.1   20.9 / 19.5
+//     11008           12.9 / 14.9   15.4 / 17.1   25.9 / 20.7   27.0 / 24.2   38.2 / 33.1   51.2 / 42.6
+// So for one token the two are equal from 8192 rows on, give or take the columns, and with 16 tokens tiles take over
+// between 4096 and 6144 rows: the cut goes by one token, and costs 16 up to a quarter between 6144 and 8192 rows.
 inline bool int8_by_rows(int64_t rows, int64_t tokens) { return tokens <= 16 && rows <= 8192; }
 
 }  // namespace gptq

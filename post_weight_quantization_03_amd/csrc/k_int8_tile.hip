@@ -12,11 +12,13 @@
 // before the barrier), and the stage BUFS on is brought into it at once; else that waits for a stage.
 //
 // Measured (tokens x columns x rows): 4096 x 11008 x 4096 160 us (2.31 POP/s, 256 x 256 tiles), a library's
-// product of the same operands 152 to 161; 8192^3 455 us (2.42), 440 to 462.  What bounds it is power: the matrix
-// cores are busy for 58 % of the cycles at 1.69 GHz, and with operands of zeros as long at 2.27 GHz.  So, for that
-// case: products of 16 x 16 (170 us), which move half as many sums as those of 32 x 32 (180); no bank conflicts
+// product of the same operands 152 to 161; 8192^3 455 us (2.42), 440 to 462.  What bounds it is power: the first keeps
+// the matrix cores busy for 62 % of 2.84e5 cycles at 1.78 GHz (159 us), with operands of zeros for 61 % of 2.89e5 at
+// 2.32 GHz (124 us).  So, for that case: products of 16 x 16 (170 us), which move half as many sums as those of 32 x 32 (180); no bank conflicts
 // (164); waves of few rows and many tokens, as rows have to be made signed (160); and nothing by a pipeline that
-// only saves cycles (177 to 180 with any of four, before these).  Requests of 128 bytes of a row: with 64-byte ones
+// only saves cycles (177 to 180 with any of four, before these).  A call that leaves places empty is bound otherwise: 1531 x 4100 x 4099
+// (204 tiles of 256 x 128 for 256 CUs, 36 to 40 us) runs at 2.5 GHz, the matrix cores of the CUs with a tile busy for
+// 37 % of the cycles: a stage takes 1.0 us there, 0.4 of them products, and 49 KB a CU out of the L2s (10 TB/s).  Requests of 128 bytes of a row: with 64-byte ones
 // tiles of 256 x 128 took 211 us instead of 177 (256 x 256 has no room in LDS for them).  Small tiles are bound by
 // the stage's chain of wait, barrier and LDS reads (0.2 to 0.4 us), so theirs are 256 columns (64 x 4096 x 4096:
 // 8.0 us, with 128 9.5), and by what the CUs read out of the L2s, 15 to 20 TB/s: with twice the waves, each half of

@@ -32,7 +32,10 @@ int64_t product(int64_t a, int64_t b) { return a != 0 && b > INT64_MAX / a ? INT
 //                 128       297 / 434     95 / 139    46 / 59    four prompts of 1024 tokens 277 / 209
 // fp32 keeps two parts of queries and weights in registers: at dim 128 its tiles of 32 rows and its 4 waves of
 // 32 spill, and so do forms that are kept, by bytes a lane: 8 waves of dim 128 in fp32 68, 4 waves of dim 128 in
-// bf16 20, of dim 256 116 in bf16 and 452 in fp32.  dim 256 fits 16 rows, or 4 waves of 32; in fp32 its rule is bf16's, which
+// bf16 20, of dim 256 116 in bf16 and 452 in fp32.  With masks: the same, but 4 waves of dim 128 in bf16 40, of dim 256
+// in fp32 388, and tiles of 32 rows of dim 128 in bf16 56, in the loop (without masks none): 13 drafted tokens, 32 over
+// 8 heads, over 30000 take 44 us where 13 tokens without a tree take 39, in 8 sequences 218 and 170; with tiles of 16 rows
+// 62 and 285, but over 700 tokens 12 instead of 16, so there the rule is the plain form's.  dim 256 fits 16 rows, or 4 waves of 32; in fp32 its rule is bf16's, which
 // gains in several short prompts and costs other calls a fifth to a half.
 int tile_rows_for(int64_t rows, int dim, bool bf16) {
   if (dim == 256) return rows <= 64 ? 16 : 128;

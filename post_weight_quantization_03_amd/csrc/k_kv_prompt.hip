@@ -483,7 +483,10 @@ __global__ __launch_bounds__(64 * NW, DIM == 256 ? 1 : 2) void k_kv_prompt(KvAtt
       const int t = t0 + PT * tile;
       // one condition of vector registers, though it is the same in all lanes: as a scalar branch the compiler reads
       // ahead across it, and spills (188 bytes a lane at dim 128)
-      if constexpr (MASKED && DIM == 256) {  // with both bodies it spills scalars between them
+      // One body where MASKED at dim 256.  It spills 80 scalars and 116 bytes a lane in bf16, 388 in fp32, with both 31,
+      // 124 and 444.  fp32 gains by it (4099 tokens, a window of 1024 and 4 first tokens, 16 over 4 heads: 367 us, with
+      // both 410; trees of 16 x 64 over 8192 775 and 819), bf16 loses (216, with both 178; 420 and 316).
+      if constexpr (MASKED && DIM == 256) {
         softmax.template operator()<true>(tile, x);
         return;
       }
